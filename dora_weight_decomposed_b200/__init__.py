@@ -13,6 +13,10 @@ every call raises.
     W_merged     = dora_merge(W0, A, B, g, s)
     B_vera       = dora_vera_compose(B_shared, b, d)       # DVoRA: B' for the calls above
     db, dd       = dora_vera_grad(B_shared, b, d, dB)
+    wq, w_scale  = dora_fp8_quantize(W_merged, block="tile")      # merged and frozen layers in 8 bits (fp8.py)
+    y, dx        = dora_fp8_forward(x, wq, w_scale), dora_fp8_backward(dy, wq, w_scale)
+    opt          = DoraAdamW([A, B, m], [dA, dB, dm], lr=1e-4)    # the update (adamw.py)
+    grad_norm    = opt.step(max_norm=1.0)
 
 bf16 tensors use the tcgen05 tensor-core path; fp32 tensors use the SIMT path.
 """
@@ -30,7 +34,8 @@ __all__ = ["DoraError", "load_library", "library_path", "dora_workspace_size", "
            "dora_profile_start",
            "dora_profile_stop", "dora_profile_count", "dora_profile_read", "DORA_OP_NORM",
            "DORA_OP_FORWARD", "DORA_OP_BACKWARD", "DORA_OP_MERGE", "DORA_OP_BACKWARD_FULL", "STATUS_NAMES",
-           "EXPORTED_SYMBOLS"]
+           "EXPORTED_SYMBOLS", "dora_fp8_quantize", "dora_fp8_forward", "dora_fp8_backward",
+           "dora_fp8_workspace_size", "DORA_FP8_OP_FORWARD", "DORA_FP8_OP_BACKWARD", "DoraAdamW", "dora_grad_norm"]
 
 DORA_BF16, DORA_FP32 = 0, 1
 DORA_OP_NORM, DORA_OP_FORWARD, DORA_OP_BACKWARD, DORA_OP_MERGE, DORA_OP_BACKWARD_FULL, DORA_OP_VERA_GRAD = range(6)
@@ -40,7 +45,9 @@ EXPORTED_SYMBOLS = ("dora_workspace_size", "dora_norm", "dora_norm_noalloc", "do
                     "dora_backward_full", "dora_merge", "dora_vera_compose", "dora_vera_grad", "dora_device_status",
                     "dora_selftest_timeout",
                     "dora_profile_start", "dora_profile_stop", "dora_profile_count", "dora_profile_read",
-                    "dora_last_error", "dora_version")
+                    "dora_last_error", "dora_version", "dora_fp8_quantize", "dora_fp8_workspace_size",
+                    "dora_fp8_forward", "dora_fp8_backward", "dora_grad_norm_workspace_size", "dora_grad_norm",
+                    "dora_adamw")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -108,6 +115,21 @@ def load_library() -> ctypes.CDLL:
         lib.dora_profile_count.restype = ctypes.c_int
         lib.dora_profile_read.argtypes = [ctypes.POINTER(ProfileRecord), ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
         lib.dora_profile_read.restype = ctypes.c_int
+        INT = ctypes.c_int
+        lib.dora_fp8_quantize.argtypes = [I64, I64, INT, INT, INT, P, P, P, P]
+        lib.dora_fp8_quantize.restype = INT
+        lib.dora_fp8_workspace_size.argtypes = [P, I64, INT]
+        lib.dora_fp8_workspace_size.restype = SZ
+        lib.dora_fp8_forward.argtypes = [P, I64, P, P, P, P, P, P, SZ, P]
+        lib.dora_fp8_forward.restype = INT
+        lib.dora_fp8_backward.argtypes = lib.dora_fp8_forward.argtypes
+        lib.dora_fp8_backward.restype = INT
+        lib.dora_grad_norm_workspace_size.argtypes = [INT]
+        lib.dora_grad_norm_workspace_size.restype = SZ
+        lib.dora_grad_norm.argtypes = [P, INT, ctypes.c_float, P, P, P, SZ, P]
+        lib.dora_grad_norm.restype = INT
+        lib.dora_adamw.argtypes = [P, P, INT, P, P, P]
+        lib.dora_adamw.restype = INT
         lib.dora_last_error.argtypes = []
         lib.dora_last_error.restype = ctypes.c_char_p
         lib.dora_version.argtypes = []
@@ -411,3 +433,8 @@ def dora_vera_grad(B_shared, b, d, dB, *, s: float = 1.0, db=None, dd=None, ws=N
     _check(lib.dora_vera_grad(ctypes.byref(desc), _ptr(B_shared), _ptr(b), _ptr(d), _ptr(dB), _ptr(db), _ptr(dd),
                               _ptr(wsb), nbytes, _stream_ptr(stream)))
     return db, dd
+
+
+from .fp8 import (DORA_FP8_OP_BACKWARD, DORA_FP8_OP_FORWARD, dora_fp8_backward, dora_fp8_forward,  # noqa: E402
+                  dora_fp8_quantize, dora_fp8_workspace_size)
+from .adamw import DoraAdamW, dora_grad_norm  # noqa: E402

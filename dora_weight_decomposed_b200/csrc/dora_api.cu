@@ -13,6 +13,13 @@ static thread_local std::string t_last_error;
 
 void set_error(const std::string& msg) { t_last_error = msg; }
 
+static StatusReader g_more_status = nullptr;
+
+bool add_status_reader(StatusReader fn) {
+  g_more_status = fn;
+  return true;
+}
+
 int device_sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -466,8 +473,6 @@ Plan make_plan(const dora_desc_t& d, int64_t T, int op) {
 
 // ------------------------------------------------------------------ checks
 
-static const int64_t kMaxDim = (int64_t)65535 * 128;  // grid.y limit on 128-row tiles
-
 static bool check_desc(const dora_desc_t* d) {
   if (!d) return set_error("desc is NULL"), false;
   if (d->dtype != DORA_BF16 && d->dtype != DORA_FP32) return set_error("desc->dtype is not DORA_BF16 or DORA_FP32"), false;
@@ -482,19 +487,19 @@ static bool check_desc(const dora_desc_t* d) {
   return true;
 }
 
-static bool check_T(int64_t T) {
+bool check_T(int64_t T) {
   if (T < 0 || T > kMaxDim) return set_error("T out of range"), false;
   return true;
 }
 
-static bool check_ptr(const void* p, const char* name, size_t align) {
+bool check_ptr(const void* p, const char* name, size_t align) {
   if (!p) return set_error(std::string(name) + " is NULL"), false;
   if (reinterpret_cast<uintptr_t>(p) % align)
     return set_error(std::string(name) + " is not " + std::to_string(align) + "-byte aligned"), false;
   return true;
 }
 
-static bool check_opt_ptr(const void* p, const char* name, size_t align) {
+bool check_opt_ptr(const void* p, const char* name, size_t align) {
   return p == nullptr || check_ptr(p, name, align);
 }
 
@@ -503,6 +508,10 @@ static size_t tensor_align(const dora_desc_t* d) { return d->dtype == DORA_BF16 
 // The bf16 path runs tcgen05 kernels built for sm_100a only.
 static dora_status_t check_device(const dora_desc_t* d) {
   if (d->dtype != DORA_BF16) return DORA_OK;
+  return check_sm100("the bf16 path needs an sm_100 (B200) device");
+}
+
+dora_status_t check_sm100(const char* otherwise) {
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -512,24 +521,28 @@ static dora_status_t check_device(const dora_desc_t* d) {
     return DORA_ECUDA;
   }
   if (major != 10 || minor != 0) {
-    set_error("the bf16 path needs an sm_100 (B200) device");
+    set_error(otherwise);
     return DORA_EUNSUPPORTED;
   }
   return DORA_OK;
 }
 
 static dora_status_t check_ws(const Plan& p, const void* ws, size_t ws_bytes) {
-  if (p.total == 0) return DORA_OK;
+  return check_ws_bytes(p.total, ws, ws_bytes);
+}
+
+dora_status_t check_ws_bytes(size_t need, const void* ws, size_t ws_bytes) {
+  if (need == 0) return DORA_OK;
   if (!ws) {
-    set_error("workspace is NULL but " + std::to_string(p.total) + " bytes are needed");
+    set_error("workspace is NULL but " + std::to_string(need) + " bytes are needed");
     return DORA_EWORKSPACE;
   }
   if (reinterpret_cast<uintptr_t>(ws) % 256) {
     set_error("workspace is not 256-byte aligned");
     return DORA_EINVAL;
   }
-  if (ws_bytes < p.total) {
-    set_error("workspace has " + std::to_string(ws_bytes) + " bytes, needs " + std::to_string(p.total));
+  if (ws_bytes < need) {
+    set_error("workspace has " + std::to_string(ws_bytes) + " bytes, needs " + std::to_string(need));
     return DORA_EWORKSPACE;
   }
   return DORA_OK;
@@ -690,7 +703,10 @@ dora_status_t dora_device_status(dora_stream_t stream, unsigned int* flags_out) 
   }
   unsigned int v = 0;
   cudaError_t e = read_and_clear_device_status(reinterpret_cast<cudaStream_t>(stream), &v);
+  unsigned int more = 0;
+  if (e == cudaSuccess && g_more_status) e = g_more_status(&more);
   if (e != cudaSuccess) return cuda_status(e, "dora_device_status");
+  v |= more;
   *flags_out = v;
   if (v) {
     set_error("a kernel's bounded wait ran out");

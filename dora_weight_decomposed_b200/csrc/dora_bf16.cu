@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "dora_internal.h"
+#include "host_launch.h"
 #include "gemm_sm100.cuh"
 #include "gram_sm100.cuh"
 #include "grouped_sm100.cuh"
@@ -33,23 +34,6 @@ namespace dora {
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ============================================================== tensor maps
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 // Row-major bf16 matrix [rows x cols], leading dimension ld elements.
 struct Mat {
@@ -84,31 +68,6 @@ static bool make_map(CUtensorMap* map, const Mat& m, int box_outer, const char* 
     return false;
   }
   return true;
-}
-
-// Launch with programmatic stream serialization so the kernel's prologue can
-// overlap the previous kernel's tail (see pdl_wait / pdl_trigger).
-template <class... KArgs, class... Args>
-static cudaError_t launch_pdl_if(bool early, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                 cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  // Under the kernel profiler each launch is timed on its own: no early start.
-  attr[0].val.programmaticStreamSerializationAllowed = (early && !profiling_on()) ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
-template <class... KArgs, class... Args>
-static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              Args&&... args) {
-  return launch_pdl_if(true, kern, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 static dora_status_t gemm_status(cudaError_t e, const char* where) {
@@ -150,20 +109,6 @@ struct GemmArgs {
   int wait_then_trigger = 0;  // see GemmGeom::wait_then_trigger
   const char* name = "gemm";
 };
-
-// Raise the kernel's dynamic shared-memory limit once per device; `done` is
-// the caller's own flag word (one per kernel instantiation).
-template <class Kern>
-static cudaError_t set_smem_once(std::atomic<unsigned long long>& done, Kern kern, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (done.load() & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit);
-  return e;
-}
 
 template <class Cfg, class Epi>
 static cudaError_t launch_gemm(const GemmArgs& g, const typename Epi::Params& ep, cudaStream_t st) {

@@ -1,0 +1,316 @@
+// Linear layers held in 8-bit floats: block quantisation, and the products
+// y = x W^T and dx = dy W with one fp32 scale per block of 128 (the kernels of
+// fp8_sm100.cuh).
+#include <algorithm>
+#include <string>
+
+#include "dora_internal.h"
+#include "fp8_sm100.cuh"
+#include "host_launch.h"
+
+namespace dora {
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// ------------------------------------------------------------------ quantisation
+
+// max(a, |b|) that keeps a NaN.
+__device__ __forceinline__ float absmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The scale of a block and its inverse. Both are powers of two, read off the
+// exponent of amax: amax = 1.f 2^x fits top = 1.75 2^k at e = x - k when
+// 1.f <= 1.75, else at x - k + 1. Non-finite: scale = amax, inverse 0 (inf) or NaN.
+struct BlockScale {
+  float scale, inv;
+};
+template <bool E5M2>
+__device__ __forceinline__ BlockScale block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u >= 0x7f800000u) return {amax, 1.0f / amax};
+  int e = (int)(u >> 23) - 127 - (E5M2 ? 15 : 8) + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, -126);
+  return {__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23)};
+}
+
+// Two values to 8-bit codes, rounded to nearest even (the scale keeps them in range; NaN stays NaN).
+template <bool E5M2>
+__device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi) {
+  uint16_t r;
+  if (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint2 to_fp8x8(const float* v, float inv) {
+  uint2 r;
+  r.x = to_fp8x2<E5M2>(v[0] * inv, v[1] * inv) | to_fp8x2<E5M2>(v[2] * inv, v[3] * inv) << 16;
+  r.y = to_fp8x2<E5M2>(v[4] * inv, v[5] * inv) | to_fp8x2<E5M2>(v[6] * inv, v[7] * inv) << 16;
+  return r;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __bfloat1622float2(h[i]);
+    v[2 * i] = t.x;
+    v[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// 1 x 128 blocks: 16 lanes of 8 values each.
+template <class T, bool E5M2>
+__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
+                                                                uint8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_trigger();
+  pdl_wait();
+  const int sub = threadIdx.x & 15;
+  const long long total = (long long)rows * nkb;
+  const long long first = (long long)blockIdx.x * 16 + (threadIdx.x >> 4), step = (long long)gridDim.x * 16;
+  const long long rounds = (total + step - 1) / step;
+  for (long long i = 0; i < rounds; ++i) {
+    const long long b = first + i * step;
+    const int row = (int)(b / nkb), kb = (int)(b % nkb);
+    const int c = kb * 128 + sub * 8;
+    const bool live = b < total && c < cols;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    if (live) load8(x + (size_t)row * cols + c, v);
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = absmax_nan(amax, v[j]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const BlockScale s = block_scale<E5M2>(amax);
+    if (live) *reinterpret_cast<uint2*>(q + (size_t)row * cols + c) = to_fp8x8<E5M2>(v, s.inv);
+    if (b < total && sub == 0) scale[(size_t)kb * rows + row] = s.scale;
+  }
+}
+
+// 128 x 128 blocks: one CTA each, 16 lanes per row, 8 rows per thread held in registers.
+template <class T, bool E5M2>
+__global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
+                                                                 uint8_t* __restrict__ q, float* __restrict__ scale) {
+  __shared__ float red[8];
+  pdl_trigger();
+  pdl_wait();
+  const int tr = blockIdx.x / nkb, tc = blockIdx.x % nkb;
+  const int c = tc * 128 + (threadIdx.x & 15) * 8, r0 = tr * 128 + (threadIdx.x >> 4);
+  float v[8][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (c < cols && r0 + 16 * i < rows) load8(x + (size_t)(r0 + 16 * i) * cols + c, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = absmax_nan(amax, v[i][j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = absmax_nan(amax, red[w]);
+  const BlockScale s = block_scale<E5M2>(amax);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c < cols && r0 + 16 * i < rows)
+      *reinterpret_cast<uint2*>(q + (size_t)(r0 + 16 * i) * cols + c) = to_fp8x8<E5M2>(v[i], s.inv);
+  if (threadIdx.x == 0) scale[blockIdx.x] = s.scale;
+}
+
+template <class T, bool E5M2>
+cudaError_t quantize_t(int64_t rows, int64_t cols, bool tiles, const void* x, void* q, float* scale, cudaStream_t st) {
+  const int nkb = (int)cdiv(cols, 128);
+  ProfRange pr(tiles ? "fp8_quantize_tiles" : "fp8_quantize_rows", st);
+  if (tiles)
+    return launch_pdl(fp8_quantize_tiles_kernel<T, E5M2>, dim3((unsigned)(cdiv(rows, 128) * nkb)), dim3(256), 0, st,
+                      (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
+  const int64_t blocks = std::min<int64_t>(cdiv(rows * nkb, 16), (int64_t)device_sm_count() * 8);
+  return launch_pdl(fp8_quantize_rows_kernel<T, E5M2>, dim3((unsigned)blocks), dim3(256), 0, st, (const T*)x,
+                    (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
+}
+
+cudaError_t quantize(int64_t rows, int64_t cols, dora_dtype_t in, dora_dtype_t fp8, bool tiles, const void* x, void* q,
+                     float* scale, cudaStream_t st) {
+  if (in == DORA_BF16)
+    return fp8 == DORA_E5M2 ? quantize_t<__nv_bfloat16, true>(rows, cols, tiles, x, q, scale, st)
+                            : quantize_t<__nv_bfloat16, false>(rows, cols, tiles, x, q, scale, st);
+  return fp8 == DORA_E5M2 ? quantize_t<float, true>(rows, cols, tiles, x, q, scale, st)
+                          : quantize_t<float, false>(rows, cols, tiles, x, q, scale, st);
+}
+
+// ------------------------------------------------------------------ products
+
+// Row-major 8-bit matrix [rows x cols] in boxes of box_rows x 128 columns, 128-byte swizzle, zeros out of bounds.
+cudaError_t make_map_u8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool B_MN>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Geom& g, cudaStream_t st) {
+  auto kern = fp8_tile_kernel<B_MN>;
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, kern, Fp8Tile<B_MN>::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
+  return launch_pdl(kern, dim3((unsigned)cdiv(g.N, 128), (unsigned)cdiv(g.T, kF8BM)), dim3(kF8Threads),
+                    Fp8Tile<B_MN>::SMEM_BYTES, st, ta, tb, g);
+}
+
+// What a call keeps in its workspace: the quantised operand and its scales.
+struct Fp8Plan {
+  size_t off_q = 0, off_s = 0, total = 0;
+};
+
+bool is_fp8(dora_dtype_t t) { return t == DORA_E4M3 || t == DORA_E5M2; }
+bool is_wide(dora_dtype_t t) { return t == DORA_BF16 || t == DORA_FP32; }
+
+Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
+  Fp8Plan p;
+  const int64_t K = op == DORA_FP8_OP_FORWARD ? d.d_in : d.d_out;
+  size_t off = 0;
+  if (!is_fp8(d.in_dtype) && T > 0) {
+    p.off_q = off;
+    off += align256((size_t)T * K);
+    p.off_s = off;
+    off += align256((size_t)T * cdiv(K, 128) * 4);
+  }
+  p.total = off;
+  return p;
+}
+
+bool check_fp8_desc(const dora_fp8_desc_t* d) {
+  if (!d) return set_error("desc is NULL"), false;
+  if (d->d_out < 1 || d->d_in < 1) return set_error("d_out and d_in must be >= 1"), false;
+  if (d->d_out > kMaxDim || d->d_in > kMaxDim) return set_error("d_out or d_in too large"), false;
+  if (d->d_out % 16 || d->d_in % 16) return set_error("8-bit layers need d_out and d_in to be multiples of 16"), false;
+  if (!is_fp8(d->in_dtype) && !is_wide(d->in_dtype)) return set_error("desc->in_dtype is not a dora_dtype_t"), false;
+  if (!is_fp8(d->in_dtype) && !is_fp8(d->fp8_dtype))
+    return set_error("desc->fp8_dtype is not DORA_E4M3 or DORA_E5M2"), false;
+  if (!is_wide(d->out_dtype)) return set_error("desc->out_dtype is not DORA_BF16 or DORA_FP32"), false;
+  return true;
+}
+
+dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, const void* x, const float* x_scale,
+                      const void* W, const float* w_scale, void* out, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!check_fp8_desc(desc) || !check_T(T)) return DORA_EINVAL;
+  const bool given = is_fp8(desc->in_dtype);
+  if (!check_ptr(W, "W", 16) || !check_ptr(w_scale, "w_scale", 4)) return DORA_EINVAL;
+  if (given ? (T > 0 && !check_ptr(x_scale, backward ? "dy_scale" : "x_scale", 4)) : x_scale != nullptr) {
+    if (!given) set_error(backward ? "dy_scale must be NULL for a bf16 or fp32 dy" : "x_scale must be NULL for a bf16 or fp32 x");
+    return DORA_EINVAL;
+  }
+  if (T > 0 && (!check_ptr(x, backward ? "dy" : "x", 16) || !check_ptr(out, backward ? "dx" : "y", 16)))
+    return DORA_EINVAL;
+  const int op = backward ? DORA_FP8_OP_BACKWARD : DORA_FP8_OP_FORWARD;
+  const Fp8Plan p = fp8_plan(*desc, T, op);
+  dora_status_t s = check_ws_bytes(p.total, ws, ws_bytes);
+  if (s != DORA_OK) return s;
+  if ((s = check_sm100("the 8-bit products need an sm_100 (B200) device")) != DORA_OK) return s;
+  if (T == 0) return DORA_OK;
+  const char* where = backward ? "dora_fp8_backward" : "dora_fp8_forward";
+  const int64_t K = backward ? desc->d_out : desc->d_in, N = backward ? desc->d_in : desc->d_out;
+  dora_dtype_t type = desc->in_dtype;
+  if (!given) {
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+    type = desc->fp8_dtype;
+    const cudaError_t e = quantize(T, K, desc->in_dtype, type, false, x, w + p.off_q, reinterpret_cast<float*>(w + p.off_s), st);
+    if (e != cudaSuccess) return cuda_status(e, where);
+    x = w + p.off_q;
+    x_scale = reinterpret_cast<const float*>(w + p.off_s);
+  }
+  const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
+  Fp8Geom g{x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
+            desc->out_dtype == DORA_FP32, type == DORA_E5M2};
+  CUtensorMap ta, tb;
+  cudaError_t e = make_map_u8(&ta, x, T, K, kF8BM);
+  if (e == cudaSuccess) e = make_map_u8(&tb, W, desc->d_out, desc->d_in, 128);
+  if (e == cudaSuccess) e = backward ? launch_tiles<true>(ta, tb, g, st) : launch_tiles<false>(ta, tb, g, st);
+  return cuda_status(e, where);
+}
+
+// After the stream is synchronised: the kernels' timeout flags, cleared.
+cudaError_t read_and_clear_status(unsigned int* out) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (v) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero));
+  }
+  *out = v;
+  return e;
+}
+
+const bool status_added = add_status_reader(read_and_clear_status);
+
+}  // namespace
+}  // namespace dora
+
+using namespace dora;
+
+extern "C" {
+
+dora_status_t dora_fp8_quantize(int64_t rows, int64_t cols, dora_dtype_t in_dtype, dora_dtype_t fp8_dtype,
+                                dora_fp8_block_t block, const void* x, void* q, float* scale, dora_stream_t stream) {
+  if (rows < 0 || cols < 1 || rows > kMaxDim || cols > kMaxDim) return set_error("rows or cols out of range"), DORA_EINVAL;
+  if (cols % 16) return set_error("cols must be a multiple of 16"), DORA_EINVAL;
+  if (!is_wide(in_dtype)) return set_error("in_dtype is not DORA_BF16 or DORA_FP32"), DORA_EINVAL;
+  if (!is_fp8(fp8_dtype)) return set_error("fp8_dtype is not DORA_E4M3 or DORA_E5M2"), DORA_EINVAL;
+  if (block != DORA_FP8_ROWS && block != DORA_FP8_TILES) return set_error("block is not a dora_fp8_block_t"), DORA_EINVAL;
+  if (cdiv(rows, 128) * cdiv(cols, 128) > INT32_MAX) return set_error("matrix too large"), DORA_EINVAL;
+  if (rows == 0) return DORA_OK;
+  if (!check_ptr(x, "x", 16) || !check_ptr(q, "q", 16) || !check_ptr(scale, "scale", 4)) return DORA_EINVAL;
+  const dora_status_t s = check_sm100("the 8-bit calls need an sm_100 (B200) device");
+  if (s != DORA_OK) return s;
+  return cuda_status(quantize(rows, cols, in_dtype, fp8_dtype, block == DORA_FP8_TILES, x, q, scale,
+                              reinterpret_cast<cudaStream_t>(stream)),
+                     "dora_fp8_quantize");
+}
+
+size_t dora_fp8_workspace_size(const dora_fp8_desc_t* desc, int64_t T, int op) {
+  if (!check_fp8_desc(desc) || !check_T(T) || op < DORA_FP8_OP_FORWARD || op > DORA_FP8_OP_BACKWARD) return 0;
+  return fp8_plan(*desc, T, op).total;
+}
+
+dora_status_t dora_fp8_forward(const dora_fp8_desc_t* desc, int64_t T, const void* x, const float* x_scale,
+                               const void* W, const float* w_scale, void* y, void* ws, size_t ws_bytes,
+                               dora_stream_t stream) {
+  return product(false, desc, T, x, x_scale, W, w_scale, y, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dora_status_t dora_fp8_backward(const dora_fp8_desc_t* desc, int64_t T, const void* dy, const float* dy_scale,
+                                const void* W, const float* w_scale, void* dx, void* ws, size_t ws_bytes,
+                                dora_stream_t stream) {
+  return product(true, desc, T, dy, dy_scale, W, w_scale, dx, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

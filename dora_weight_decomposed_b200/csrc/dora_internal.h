@@ -70,8 +70,20 @@ Plan make_plan(const dora_desc_t& d, int64_t T, int op);
 // Thread-local error message for dora_last_error().
 void set_error(const std::string& msg);
 
+// Argument checks shared by the calls: each sets the error message where it refuses.
+constexpr int64_t kMaxDim = int64_t(65535) * 128;  // grid.y limit on 128-row tiles
+bool check_T(int64_t T);
+bool check_ptr(const void* p, const char* name, size_t align);
+bool check_opt_ptr(const void* p, const char* name, size_t align);
+dora_status_t check_ws_bytes(size_t need, const void* ws, size_t ws_bytes);
+dora_status_t check_sm100(const char* otherwise);
+
 // Status word written by kernels whose bounded waits ran out.
 cudaError_t read_and_clear_device_status(cudaStream_t st, unsigned int* out);
+// The 8-bit products' kernels have a status word of their own (no relocatable device code):
+// their translation unit hands its reader over when the library loads.
+using StatusReader = cudaError_t (*)(unsigned int* out);
+bool add_status_reader(StatusReader fn);
 // One kernel whose bounded wait runs out after limit_us (failure-detection test).
 dora_status_t selftest_timeout(uint32_t limit_us, unsigned int* scratch, cudaStream_t st);
 

@@ -180,6 +180,17 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
+// The same for 8-bit floats (e4m3 / e5m2, chosen per operand in idesc): 32 K values per instruction.
+__device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on bar when every tcgen05.mma issued so far by this thread is done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -319,6 +330,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          | (1u << 7)                               // A format: bf16
          | (1u << 10)                              // B format: bf16
          | ((a_mn ? 1u : 0u) << 15)                // A major
+         | ((b_mn ? 1u : 0u) << 16)                // B major
+         | ((uint32_t)(N >> 3) << 17)              // N / 8
+         | ((uint32_t)(M >> 4) << 24);             // M / 16
+}
+
+// Instruction descriptor for kind::f8f6f4 with an fp32 accumulator; e5m2 instead of e4m3 where set.
+__host__ __device__ constexpr uint32_t idesc_fp8_f32(int M, int N, bool a_e5m2, bool b_e5m2, bool b_mn) {
+  return (1u << 4)                                 // D format: f32
+         | ((a_e5m2 ? 1u : 0u) << 7)               // A format
+         | ((b_e5m2 ? 1u : 0u) << 10)              // B format
          | ((b_mn ? 1u : 0u) << 16)                // B major
          | ((uint32_t)(N >> 3) << 17)              // N / 8
          | ((uint32_t)(M >> 4) << 24);             // M / 16

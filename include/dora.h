@@ -9,8 +9,11 @@
  *
  * Calls: dora_norm, dora_forward, dora_backward (the layer step);
  * dora_backward_full (without the norm's detach), dora_merge (deployment
- * weight), dora_vera_compose / dora_vera_grad (DVoRA); workspace sizing,
- * device status, a failure-detection self-test and kernel timing.
+ * weight), dora_vera_compose / dora_vera_grad (DVoRA); dora_fp8_quantize /
+ * dora_fp8_forward / dora_fp8_backward (merged and frozen layers held in 8
+ * bits); dora_grad_norm / dora_adamw (the update of the trained tensors);
+ * workspace sizing, device status, a failure-detection self-test and kernel
+ * timing.
  *
  * Sources: "DoRA 阅读笔记" (zhongzhuzhou.org reading notes on DoRA, arXiv
  * 2402.09353) eq. (1), eq. (6), Algorithm 1, eq. (7), eq. (8), sections 3.4
@@ -64,7 +67,8 @@ typedef enum {
   DORA_ETIMEOUT = 5       /* a kernel's bounded wait ran out (see dora_device_status) */
 } dora_status_t;
 
-typedef enum { DORA_BF16 = 0, DORA_FP32 = 1 } dora_dtype_t;
+/* The 8-bit floats appear in the dora_fp8_* calls only. */
+typedef enum { DORA_BF16 = 0, DORA_FP32 = 1, DORA_E4M3 = 2, DORA_E5M2 = 3 } dora_dtype_t;
 
 typedef enum {
   DORA_OP_NORM = 0,
@@ -231,6 +235,134 @@ DORA_API dora_status_t dora_vera_grad(const dora_desc_t* desc, const void* B_sha
  */
 DORA_API dora_status_t dora_merge(const dora_desc_t* desc, const void* W0, const void* A, const void* B,
                                   const float* g, void* W_out, void* ws, size_t ws_bytes, dora_stream_t stream);
+
+/*
+ * Linear layers held in 8-bit floats, with one fp32 scale per block of 128:
+ * a merged weight (dora_merge) that is served, or a frozen layer beside the
+ * adapted ones in training. The weight is W = w_scale (.) wq in 128 x 128
+ * blocks; the other operand (x, or dy) is scaled in 1 x 128 blocks along the
+ * contracted dimension. Every pointer is 16-byte aligned.
+ *
+ * dora_fp8_quantize: q and scale of a row-major matrix x [rows x cols] (bf16
+ *   or fp32). cols is a multiple of 16; a last block may be partial.
+ *     amax  = max |x| of the block (NaN if it holds a NaN)
+ *     scale = 2^e, e >= -126 the smallest integer with amax <= top 2^e (top =
+ *             448 for e4m3, 57344 for e5m2); a non-finite amax is its own scale
+ *     q     = x / scale rounded to nearest, ties to even
+ *   A power of two divides exactly, so each value is rounded once.
+ *   block DORA_FP8_ROWS:  1 x 128 blocks, scale [ceil(cols / 128)][rows]
+ *   block DORA_FP8_TILES: 128 x 128 blocks, scale [ceil(rows / 128)][ceil(cols / 128)]
+ *
+ * dora_fp8_forward:  y = x W^T for T tokens, x [T x d_in], y [T x d_out].
+ *     y[t][n] = sum_kb x_scale[kb][t] w_scale[n / 128][kb] sum_{k in kb} xq[t][k] wq[n][k]
+ * dora_fp8_backward: dx = dy W, the input gradient (the weight is frozen and
+ *   gets none), dy [T x d_out], dx [T x d_in].
+ *     dx[t][k] = sum_nb dy_scale[nb][t] w_scale[nb][k / 128] sum_{n in nb} dyq[t][n] wq[n][k]
+ *   Sums are fp32; each result is rounded once to out_dtype (bf16 or fp32).
+ *   in_dtype bf16 or fp32: the operand is quantised in the call to fp8_dtype
+ *   in 1 x 128 blocks (x_scale must be NULL). in_dtype e4m3 or e5m2: it comes
+ *   quantised, with the scales of DORA_FP8_ROWS (fp8_dtype is not read).
+ *   Any fp32 scales are taken, not only powers of two. W is e4m3 [d_out x
+ *   d_in] with the scales of DORA_FP8_TILES. d_out and d_in are multiples of
+ *   16; T may be any value >= 0 (T = 0 does nothing).
+ *   Workspace: dora_fp8_workspace_size (0 for an invalid descriptor).
+ */
+typedef enum { DORA_FP8_ROWS = 0, DORA_FP8_TILES = 1 } dora_fp8_block_t;
+typedef enum { DORA_FP8_OP_FORWARD = 0, DORA_FP8_OP_BACKWARD = 1 } dora_fp8_op_t;
+
+typedef struct {
+  int64_t d_out;          /* rows of W    */
+  int64_t d_in;           /* columns of W */
+  dora_dtype_t in_dtype;  /* of x (forward) or dy (backward) */
+  dora_dtype_t fp8_dtype; /* what a bf16 or fp32 operand is quantised to */
+  dora_dtype_t out_dtype; /* of y or dx */
+} dora_fp8_desc_t;
+
+DORA_API dora_status_t dora_fp8_quantize(int64_t rows, int64_t cols, dora_dtype_t in_dtype, dora_dtype_t fp8_dtype,
+                                         dora_fp8_block_t block, const void* x, void* q, float* scale,
+                                         dora_stream_t stream);
+DORA_API size_t dora_fp8_workspace_size(const dora_fp8_desc_t* desc, int64_t T, int op);
+DORA_API dora_status_t dora_fp8_forward(const dora_fp8_desc_t* desc, int64_t T, const void* x, const float* x_scale,
+                                        const void* W, const float* w_scale, void* y, void* ws, size_t ws_bytes,
+                                        dora_stream_t stream);
+DORA_API dora_status_t dora_fp8_backward(const dora_fp8_desc_t* desc, int64_t T, const void* dy,
+                                         const float* dy_scale, const void* W, const float* w_scale, void* dx,
+                                         void* ws, size_t ws_bytes, dora_stream_t stream);
+
+/*
+ * The update of the trained tensors (A, B and m of every adapted layer) from
+ * the gradients of dora_backward, for many tensors in one call.
+ *
+ * dora_grad_norm: the global norm of n_tensors gradients and the scale that
+ *   clips them to max_norm:
+ *     norm  = sqrt(sum over all tensors of g^2)
+ *     scale = min(1, max_norm / (norm + 1e-6)); NaN when the norm is not finite
+ *   max_norm = +inf gives scale 1. norm and scale are one fp32 each in device
+ *   memory. Sums are taken in double above 256 values, in a fixed order.
+ *   Workspace: dora_grad_norm_workspace_size(n_tensors).
+ *
+ * dora_adamw: one AdamW step t = control->step + 1,
+ *     g' = grad_scale g      (grad_scale NULL: 1)
+ *     m' = beta1 m + (1 - beta1) g',   v' = beta2 v + (1 - beta2) g'^2
+ *     p' = p - lr wd p - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ *   in fp32 whatever the tensors' type. A master copy (fp32) holds p where
+ *   given; param is then p' rounded to nearest. state_bits = 32: exp_avg = m
+ *   and exp_avg_sq = v in fp32. state_bits = 8: exp_avg holds m and exp_avg_sq
+ *   holds sqrt(v) as e4m3 codes in blocks of 128 consecutive elements, value =
+ *   code * scale[block], scale = max(amax / 448, 2^-126); the step uses m' and
+ *   v' before they are rounded. Codes are rounded stochastically, down or up
+ *   with the probability that keeps the mean (a moment moves by 1 - beta of
+ *   itself a step, far less than a code: rounding to nearest would freeze it),
+ *   with 16 random bits per element hashed from (seed, t, (index0 + i) / 2);
+ *   a nonzero v' is never held as code zero.
+ *   control is device memory of the caller: step, the count of steps done (the
+ *   call adds one), lr, and an internal counter that starts at 0 and is 0
+ *   between calls. All of it is read when the kernels run, so a captured call
+ *   replays as further steps. A grad_scale that is not finite skips the step:
+ *   nothing is written, the count included.
+ *   tensors and dora_grad_t arrays are host memory, read before the call
+ *   returns. exp_avg, exp_avg_sq and master are 16-byte aligned, param and
+ *   grad to their element size. Tensors must not overlap. No workspace.
+ */
+typedef struct {
+  const void* grad;
+  int64_t numel;
+  dora_dtype_t dtype; /* bf16 or fp32 */
+} dora_grad_t;
+
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* scale_avg;      /* state_bits = 8: [ceil(numel / 128)], else not read */
+  float* scale_sq;
+  float* master;         /* fp32 copy of param, or NULL */
+  int64_t numel;
+  int64_t index0;        /* first element's place in the random sequence, a multiple of 8 */
+  float weight_decay;
+  dora_dtype_t param_dtype; /* bf16 or fp32 */
+  dora_dtype_t grad_dtype;
+} dora_adamw_tensor_t;
+
+typedef struct {
+  int64_t step;
+  float lr;
+  uint32_t counter;
+} dora_adamw_control_t;
+
+typedef struct {
+  double beta1, beta2;
+  float eps;
+  int state_bits;   /* 32 or 8 */
+  uint32_t seed;
+} dora_adamw_desc_t;
+
+DORA_API size_t dora_grad_norm_workspace_size(int n_tensors);
+DORA_API dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, float max_norm, float* norm,
+                                      float* scale, void* ws, size_t ws_bytes, dora_stream_t stream);
+DORA_API dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
+                                  dora_adamw_control_t* control, const float* grad_scale, dora_stream_t stream);
 
 /*
  * dora_device_status -- synchronise `stream`, then read and clear the library's
