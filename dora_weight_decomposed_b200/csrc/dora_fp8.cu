@@ -185,6 +185,17 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
                     Fp8Tile<B_MN>::SMEM_BYTES, st, ta, tb, g);
 }
 
+template <bool B_MN>
+cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Geom& g, cudaStream_t st) {
+  auto kern = fp8_pair_kernel<B_MN>;
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, kern, kF8PairSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::min<int64_t>(cdiv(g.T, 256) * cdiv(g.N, 256), std::max(1, device_sm_count() / 2));
+  ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
+  return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, g);
+}
+
 // What a call keeps in its workspace: the quantised operand and its scales.
 struct Fp8Plan {
   size_t off_q = 0, off_s = 0, total = 0;
@@ -253,7 +264,12 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   CUtensorMap ta, tb;
   cudaError_t e = make_map_u8(&ta, x, T, K, kF8BM);
   if (e == cudaSuccess) e = make_map_u8(&tb, W, desc->d_out, desc->d_in, 128);
-  if (e == cudaSuccess) e = backward ? launch_tiles<true>(ta, tb, g, st) : launch_tiles<false>(ta, tb, g, st);
+  if (e == cudaSuccess) {
+    if (T > 128)
+      e = backward ? launch_pairs<true>(ta, tb, g, st) : launch_pairs<false>(ta, tb, g, st);
+    else
+      e = backward ? launch_tiles<true>(ta, tb, g, st) : launch_tiles<false>(ta, tb, g, st);
+  }
   return cuda_status(e, where);
 }
 
