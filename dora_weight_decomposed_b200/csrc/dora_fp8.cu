@@ -57,52 +57,88 @@ __device__ __forceinline__ uint2 to_fp8x8(const float* v, float inv) {
   return r;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(h[i]);
-    v[2 * i] = t.x;
-    v[2 * i + 1] = t.y;
+// Eight consecutive values as they lie in memory (a bf16 thread holds half the registers that fp32 would take).
+struct Raw8Bf16 {
+  uint4 u;
+  __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ void clear() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ float absmax() const {  // NaN if one is
+    uint32_t m;
+    asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"
+        : "=r"(m)
+        : "r"(u.x & 0x7fff7fffu), "r"(u.y & 0x7fff7fffu), "r"(u.z & 0x7fff7fffu), "r"(u.w & 0x7fff7fffu));
+    return absmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
-}
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+  __device__ void values(float* v) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+struct Raw8Float {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ float absmax() const {
+    float v[8], m = 0.f;
+    values(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = absmax_nan(m, v[i]);
+    return m;
+  }
+  __device__ void values(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <class T>
+struct Raw8 : Raw8Float {};
+template <>
+struct Raw8<__nv_bfloat16> : Raw8Bf16 {};
 
-// 1 x 128 blocks: 16 lanes of 8 values each.
+// 1 x 128 blocks. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
+// in flight; the CTA's eight warps take neighbouring column blocks. Bound by HBM.
 template <class T, bool E5M2>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                 uint8_t* __restrict__ q, float* __restrict__ scale) {
   pdl_trigger();
   pdl_wait();
-  const int sub = threadIdx.x & 15;
-  const long long total = (long long)rows * nkb;
-  const long long first = (long long)blockIdx.x * 16 + (threadIdx.x >> 4), step = (long long)gridDim.x * 16;
-  const long long rounds = (total + step - 1) / step;
-  for (long long i = 0; i < rounds; ++i) {
-    const long long b = first + i * step;
-    const int row = (int)(b / nkb), kb = (int)(b % nkb);
-    const int c = kb * 128 + sub * 8;
-    const bool live = b < total && c < cols;
-    float v[8];
+  const int kb = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (kb >= nkb) return;
+  const int sub = threadIdx.x & 15, h = (threadIdx.x >> 4) & 1;
+  const int c = kb * 128 + sub * 8, r0 = blockIdx.x * 16 + h;
+  const size_t at = (size_t)r0 * cols + c;
+  Raw8<T> raw[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    if (live) load8(x + (size_t)row * cols + c, v);
-    float amax = 0.f;
+  for (int i = 0; i < 8; ++i) {
+    if (c < cols && r0 + 2 * i < rows)
+      raw[i].load(x + at + (size_t)(2 * i) * cols);
+    else
+      raw[i].clear();
+  }
+  float mine = 0.f;  // lane `sub` keeps the scale of its half's row `sub`, so that 16 rows' scales are stored together
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = absmax_nan(amax, v[j]);
+  for (int i = 0; i < 8; ++i) {
+    float amax = raw[i].absmax();
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const BlockScale s = block_scale<E5M2>(amax);
-    if (live) *reinterpret_cast<uint2*>(q + (size_t)row * cols + c) = to_fp8x8<E5M2>(v, s.inv);
-    if (b < total && sub == 0) scale[(size_t)kb * rows + row] = s.scale;
+    if (sub == i) mine = s.scale;
+    float v[8];
+    raw[i].values(v);
+    if (c < cols && r0 + 2 * i < rows)
+      *reinterpret_cast<uint2*>(q + at + (size_t)(2 * i) * cols) = to_fp8x8<E5M2>(v, s.inv);
   }
+  if (sub < 8 && r0 + 2 * sub < rows) scale[(size_t)kb * rows + r0 + 2 * sub] = mine;
 }
 
-// 128 x 128 blocks: one CTA each, 16 lanes per row, 8 rows per thread held in registers.
+// 128 x 128 blocks: one CTA each, 16 lanes per row, 8 rows per thread held in registers between the maximum and the
+// codes, so that the matrix is read once. Bound by HBM.
 template <class T, bool E5M2>
 __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                  uint8_t* __restrict__ q, float* __restrict__ scale) {
@@ -111,18 +147,18 @@ __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __rest
   pdl_wait();
   const int tr = blockIdx.x / nkb, tc = blockIdx.x % nkb;
   const int c = tc * 128 + (threadIdx.x & 15) * 8, r0 = tr * 128 + (threadIdx.x >> 4);
-  float v[8][8];
-  float amax = 0.f;
+  const size_t at = (size_t)r0 * cols + c;
+  Raw8<T> raw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (c < cols && r0 + 16 * i < rows) load8(x + (size_t)(r0 + 16 * i) * cols + c, v[i]);
+    if (c < cols && r0 + 16 * i < rows)
+      raw[i].load(x + at + (size_t)(16 * i) * cols);
+    else
+      raw[i].clear();
   }
+  float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = absmax_nan(amax, v[i][j]);
+  for (int i = 0; i < 8; ++i) amax = absmax_nan(amax, raw[i].absmax());
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
@@ -131,9 +167,12 @@ __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __rest
   for (int w = 0; w < 8; ++w) amax = absmax_nan(amax, red[w]);
   const BlockScale s = block_scale<E5M2>(amax);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    raw[i].values(v);
     if (c < cols && r0 + 16 * i < rows)
-      *reinterpret_cast<uint2*>(q + (size_t)(r0 + 16 * i) * cols + c) = to_fp8x8<E5M2>(v[i], s.inv);
+      *reinterpret_cast<uint2*>(q + at + (size_t)(16 * i) * cols) = to_fp8x8<E5M2>(v, s.inv);
+  }
   if (threadIdx.x == 0) scale[blockIdx.x] = s.scale;
 }
 
@@ -144,9 +183,8 @@ cudaError_t quantize_t(int64_t rows, int64_t cols, bool tiles, const void* x, vo
   if (tiles)
     return launch_pdl(fp8_quantize_tiles_kernel<T, E5M2>, dim3((unsigned)(cdiv(rows, 128) * nkb)), dim3(256), 0, st,
                       (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
-  const int64_t blocks = std::min<int64_t>(cdiv(rows * nkb, 16), (int64_t)device_sm_count() * 8);
-  return launch_pdl(fp8_quantize_rows_kernel<T, E5M2>, dim3((unsigned)blocks), dim3(256), 0, st, (const T*)x,
-                    (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
+  return launch_pdl(fp8_quantize_rows_kernel<T, E5M2>, dim3((unsigned)cdiv(rows, 16), (unsigned)cdiv(nkb, 8)), dim3(256),
+                    0, st, (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
 }
 
 cudaError_t quantize(int64_t rows, int64_t cols, dora_dtype_t in, dora_dtype_t fp8, bool tiles, const void* x, void* q,

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 // half of the columns, 128 fp32 sums per thread, so that each scheduler issues
 // about half as many instructions as a k-block of MMAs takes clocks. Tiles
 // are walked persistently; the MMAs of the next tile start while this one is stored.
-constexpr int kF8PairThreads = 320;
+constexpr int kF8FoldWarps = 8;
+constexpr int kF8PairThreads = 64 + 32 * kF8FoldWarps;
 constexpr int kF8PairStages = 6;
 constexpr int kF8StageBytes = 2 * 128 * 128;
 constexpr int kF8PairSmem = kF8PairStages * kF8StageBytes + 256 + 1024;
@@ -235,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 16);
+      mbar_init(&acce[b], 2 * kF8FoldWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&tA);
@@ -253,8 +254,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 2) {
+    if (warp == 0 && lane == 0) {
       int it = 0;
       bool ok = true;
 #pragma unroll 1
@@ -283,9 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
         for (int j = max(0, it - STAGES); j < it; ++j)
           mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, kWaitLimitNs / 16);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_fp8_f32(256, 256, g.a_e5m2 != 0, false, B_MN);
       constexpr uint32_t b_kstep = B_MN ? 32u * 128u : 32u;
       int it = 0;
@@ -311,8 +310,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t done[2] = {mapa_shared(smem_u32(&acce[0]), 0), mapa_shared(smem_u32(&acce[1]), 0)};
+    constexpr int COLS = 4 * 256 / kF8FoldWarps;  // columns per warp
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t done = mapa_shared(smem_u32(acce), 0);
     int it = 0;
     bool ok = true;
 #pragma unroll 1
@@ -321,46 +321,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
       fp8_tile_coords(t, m_tiles, n_tiles, tm, tn);
       const int mw = tm * 256 + (int)rank * 128 + q * 32;  // first row of the warp
       const int m = mw + lane;
-      const int n0 = tn * 256 + half * 128;
+      const int n0 = tn * 256 + part * COLS;
       const bool live = mw < g.T && n0 < g.N;  // of the warp
       const float* xs = g.xs + min(m, g.T - 1);
       const float* ws = g.ws + (live ? (size_t)(n0 >> 7) * g.ws_n : 0);
-      float2 acc[64];
+      float2 acc[COLS / 2];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // Scales are fetched two k-blocks ahead.
-      float s0 = xs[0] * ws[0], s1 = 0.f;
-      if (g.nkb > 1) s1 = xs[(size_t)g.T] * ws[g.ws_k];
+      for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      // Scales are fetched two k-blocks ahead and multiplied where they are used, so that nothing waits for them.
+      float x0 = xs[0], w0 = ws[0], x1 = 0.f, w1 = 0.f;
+      if (g.nkb > 1) x1 = xs[(size_t)g.T], w1 = ws[g.ws_k];
 #pragma unroll 1
       for (int kb = 0; kb < g.nkb; ++kb, ++it) {
         const int b = it & 1;
-        const float s = s0;
-        s0 = s1;
-        if (kb + 2 < g.nkb) s1 = xs[(size_t)(kb + 2) * g.T] * ws[(size_t)(kb + 2) * g.ws_k];
+        const float s = x0 * w0;
+        x0 = x1, w0 = w1;
+        if (kb + 2 < g.nkb) x1 = xs[(size_t)(kb + 2) * g.T], w1 = ws[(size_t)(kb + 2) * g.ws_k];
         if (!mbar_wait(&accf[b], (uint32_t)(it >> 1) & 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (live) {
-          const uint32_t ta = tmem + b * 256u + half * 128u + ((uint32_t)(q * 32) << 16);
-          uint32_t v[2][16];
-          tmem_ld16_async(ta, v[0]);
+          const uint32_t ta = tmem + b * 256u + part * COLS + ((uint32_t)(q * 32) << 16);
+          uint32_t v[16];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < COLS / 16; ++c) {
+            tmem_ld16_async(ta + c * 16, v);
             tmem_ld_wait();
-            if (c < 7) tmem_ld16_async(ta + (c + 1) * 16, v[(c + 1) & 1]);
+            if (c == COLS / 16 - 1) {  // the accumulator is read: the MMAs may have it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(done + 8 * b);
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s);
+            for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], v[2 * j], v[2 * j + 1], s);
           }
+        } else if (lane == 0) {
+          mbar_arrive_cluster(done + 8 * b);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(done[b]);
       }
       if (ok && live && m < g.T) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) fp8_store32(g, m, n0 + c * 32, reinterpret_cast<const float*>(acc) + c * 32);
+        for (int c = 0; c < COLS / 32; ++c) fp8_store32(g, m, n0 + c * 32, reinterpret_cast<const float*>(acc) + c * 32);
       }
     }
   }
