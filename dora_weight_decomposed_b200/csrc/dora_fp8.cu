@@ -101,13 +101,14 @@ struct Raw8 : Raw8Float {};
 template <>
 struct Raw8<__nv_bfloat16> : Raw8Bf16 {};
 
-// 1 x 128 blocks. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
+// 1 x 128 blocks. It lets the next grid start only once all work before it is done, so that a product which
+// follows it may read the weight at once. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
 // in flight; the CTA's eight warps take neighbouring column blocks. Bound by HBM.
 template <class T, bool E5M2>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                 uint8_t* __restrict__ q, float* __restrict__ scale) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int kb = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (kb >= nkb) return;
   const int sub = threadIdx.x & 15, h = (threadIdx.x >> 4) & 1;
@@ -212,15 +213,94 @@ cudaError_t make_map_u8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool B_MN>
-cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Geom& g, cudaStream_t st) {
-  auto kern = fp8_tile_kernel<B_MN>;
+// Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
+// answer of the occupancy query, which counts one CTA per SM for the narrow kernels; asked once per device.
+template <int NT, bool W_MN>
+int clusters_alone(int cs) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) dev = 63;
+  int n = known[dev][cs].load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cs * 1024u);
+    cfg.blockDim = dim3(kF8Threads);
+    cfg.dynamicSmemBytes = Fp8Narrow<NT>::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = std::max(1, device_sm_count() / cs * 7 / 8);
+    }
+    n = std::min(n, std::max(1, device_sm_count() / cs));
+    known[dev][cs].store(n);
+  }
+  return n;
+}
+
+// The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two, and 256
+// CTAs of one launch were seen to start together): twice as many, or one on every (cs + 1) / 2 SMs.
+template <int NT, bool W_MN>
+int narrow_slots(int cs) {
+  return std::max(2 * clusters_alone<NT, W_MN>(cs), clusters_alone<NT, W_MN>((cs + 1) / 2));
+}
+
+// CTAs per tile of the narrow kernel (K splits, one cluster): the count with the least estimated time, in k-blocks:
+// waves of clusters times the k-blocks of a split plus what a CTA costs beside them, 2 to start and fill and 2 more
+// to add the splits. T = 37 of 27648 x 5120 takes 31.3 us with its 216 tiles in one wave, 36.5 us with two splits
+// and 432 CTAs in two waves; T = 16 of 8192 x 8192 17.7 us with 4 splits (256 CTAs), 22.3 us with 8 (two waves).
+template <int NT, bool W_MN>
+int narrow_splits(int64_t tiles, int64_t nkb) {
+  int best = 1;
+  double best_t = 1e300;
+  for (int cs = 1; cs <= 8 && cs <= nkb; ++cs) {
+    const double t = (double)cdiv(tiles, narrow_slots<NT, W_MN>(cs)) * ((double)cdiv(nkb, cs) + (cs > 1 ? 4.0 : 2.0));
+    if (t < best_t - 1e-9) {
+      best_t = t;
+      best = cs;
+    }
+  }
+  return best;
+}
+
+template <int NT, bool W_MN>
+cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp8Geom& g, bool early_w, cudaStream_t st) {
+  auto kern = fp8_narrow_kernel<NT, W_MN>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, kern, Fp8Tile<B_MN>::SMEM_BYTES);
+  cudaError_t e = set_smem_once(smem_set, kern, Fp8Narrow<NT>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
-  return launch_pdl(kern, dim3((unsigned)cdiv(g.N, 128), (unsigned)cdiv(g.T, kF8BM)), dim3(kF8Threads),
-                    Fp8Tile<B_MN>::SMEM_BYTES, st, ta, tb, g);
+  const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
+  const int cs = narrow_splits<NT, W_MN>(tiles * t_tiles, g.nkb);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)t_tiles);
+  cfg.blockDim = dim3(kF8Threads);
+  cfg.dynamicSmemBytes = Fp8Narrow<NT>::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = profiling_on() ? 0 : 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  ProfRange pr(W_MN ? "fp8_backward" : "fp8_forward", st);
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, g, cs, early_w ? 1 : 0);
+}
+
+template <bool W_MN>
+cudaError_t launch_narrow_nt(int nt, const CUtensorMap& tw, const CUtensorMap& tx, const Fp8Geom& g, bool early_w,
+                             cudaStream_t st) {
+  switch (nt) {
+    case 16: return launch_narrow<16, W_MN>(tw, tx, g, early_w, st);
+    case 32: return launch_narrow<32, W_MN>(tw, tx, g, early_w, st);
+    case 64: return launch_narrow<64, W_MN>(tw, tx, g, early_w, st);
+    default: return launch_narrow<128, W_MN>(tw, tx, g, early_w, st);
+  }
 }
 
 template <bool B_MN>
@@ -299,14 +379,16 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
   Fp8Geom g{x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
             desc->out_dtype == DORA_FP32, type == DORA_E5M2};
-  CUtensorMap ta, tb;
-  cudaError_t e = make_map_u8(&ta, x, T, K, kF8BM);
-  if (e == cudaSuccess) e = make_map_u8(&tb, W, desc->d_out, desc->d_in, 128);
+  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const bool narrow = T <= 128;
+  CUtensorMap tx, tw;
+  cudaError_t e = make_map_u8(&tx, x, T, K, narrow ? nt : 128);
+  if (e == cudaSuccess) e = make_map_u8(&tw, W, desc->d_out, desc->d_in, 128);
   if (e == cudaSuccess) {
-    if (T > 128)
-      e = backward ? launch_pairs<true>(ta, tb, g, st) : launch_pairs<false>(ta, tb, g, st);
+    if (narrow)
+      e = backward ? launch_narrow_nt<true>(nt, tw, tx, g, !given, st) : launch_narrow_nt<false>(nt, tw, tx, g, !given, st);
     else
-      e = backward ? launch_tiles<true>(ta, tb, g, st) : launch_tiles<false>(ta, tb, g, st);
+      e = backward ? launch_pairs<true>(tx, tw, g, st) : launch_pairs<false>(tx, tw, g, st);
   }
   return cuda_status(e, where);
 }

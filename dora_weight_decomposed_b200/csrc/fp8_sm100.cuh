@@ -13,7 +13,6 @@
 
 namespace dora {
 
-constexpr int kF8BM = 128;  // token rows per tile
 constexpr int kF8BK = 128;  // K per block: one 128-byte swizzle row, one scale
 constexpr int kF8Threads = 192;
 
@@ -51,34 +50,86 @@ __device__ __forceinline__ void fp8_store32(const Fp8Geom& g, int m, int n, cons
   }
 }
 
-// One 128 x 128 tile per CTA. B_MN: the weight's rows run along K (the input
-// gradient reads W [d_out x d_in] with K = d_out), so its tile is MN-major.
-template <bool B_MN>
-struct Fp8Tile {
-  static constexpr int TILE_BYTES = 128 * 128;
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  static constexpr int STAGES = 6;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 256 + 1024;
+// a.xy += v.xy * s.xy: two fp32 multiply-adds in one instruction (T = 512, K = 16384 on 16 pairs: 71 us, 84 us with
+// two instructions).
+__device__ __forceinline__ void fma2(float2& a, uint32_t v0, uint32_t v1, float s0, float s1) {
+  asm("{\n\t.reg .b64 v, s, a;\n\t"
+      "mov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\tmov.b64 a, {%0, %1};\n\t"
+      "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+
+// ------------------------------------------------------------------ few tokens
+//
+// With few tokens the weight's bytes are the cost, so the operands change places: 128 rows of the weight are the
+// MMA's M, the NT tokens its N, and D holds the result transposed (lane = weight row, column = token). The K
+// blocks of a tile are split over the CTAs of a cluster so that enough of the weight is in flight on every SM; two
+// CTAs fit on one SM. Each CTA folds its k-blocks into registers; the cluster then adds the splits
+// through distributed shared memory in rank order, so the result does not depend on timing.
+// W_MN: the weight's rows run along K (the input gradient, W [d_out x d_in] with K = d_out).
+template <int NT>
+struct Fp8Narrow {
+  static constexpr int X_BYTES = NT * 128;
+  static constexpr int STAGE_BYTES = 16384 + X_BYTES;
+  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int SCALE_BYTES = 4 * 2 * NT * 4;  // per folding warp: two k-blocks' token scales
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES + 256 + 1024;
+  static constexpr uint32_t ACC_COLS = NT < 32 ? 16 : NT;  // two accumulators; TMEM comes in 32 columns at least
+  static_assert(NT * 128 * 4 <= STAGES * STAGE_BYTES, "the splits' sums fit the ring");
+  static_assert(SMEM_BYTES + 1024 <= 114 * 1024, "two CTAs per SM");
 };
 
-template <bool B_MN>
-__global__ void __launch_bounds__(kF8Threads, 1)
-    fp8_tile_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB, const Fp8Geom g) {
-  using Cfg = Fp8Tile<B_MN>;
+// The splits' sums of every CS-th token, starting with this CTA's own, added in rank order: a distributed shared
+// memory read costs hundreds of clocks, so each thread has all CS of a float4 in flight.
+template <int CS>
+__device__ __forceinline__ void fp8_reduce_splits(const Fp8Geom& g, const float* sum, int rank, int t0, int live, int n0) {
+  const int mine = (live - rank + CS - 1) / CS * 32;  // float4s of this CTA
+#pragma unroll 2
+  for (int i = threadIdx.x; i < mine; i += kF8Threads) {
+    const int t = rank + i / 32 * CS, n = i % 32 * 4;
+    float4 v[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r)
+      v[r] = *reinterpret_cast<const float4*>(CS == 1 ? sum + t * 128 + n : dsmem_ptr(sum + t * 128 + n, r));
+    float4 a = v[0];
+#pragma unroll
+    for (int r = 1; r < CS; ++r) a.x += v[r].x, a.y += v[r].y, a.z += v[r].z, a.w += v[r].w;
+    if (n0 + n >= g.N) continue;  // N is a multiple of 16
+    const size_t at = (size_t)(t0 + t) * g.N + n0 + n;
+    if (g.out_fp32) {
+      *reinterpret_cast<float4*>((float*)g.out + at) = a;
+    } else {
+      __nv_bfloat162 p[2] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w)};
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)g.out + at) = *reinterpret_cast<const uint2*>(p);
+    }
+  }
+}
+
+template <int NT, bool W_MN>
+__global__ void __launch_bounds__(kF8Threads, 2)
+    fp8_narrow_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX, const Fp8Geom g,
+                      int cs, int early_w) {
+  using Cfg = Fp8Narrow<NT>;
+  constexpr int STAGES = Cfg::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::STAGES * Cfg::STAGE_BYTES);
-  uint64_t* empty = full + Cfg::STAGES;
-  uint64_t* accf = empty + Cfg::STAGES;  // [2] accumulator complete
-  uint64_t* acce = accf + 2;             // [2] accumulator folded
+  float* scales = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE_BYTES + Cfg::SCALE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;  // [2] accumulator complete
+  uint64_t* acce = accf + 2;        // [2] accumulator folded
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_tile = blockIdx.x, m_tile = blockIdx.y;
+  const int rank = blockIdx.x % cs;  // the cluster's CTAs are neighbours in x
+  const int n0 = blockIdx.x / cs * 128, t0 = blockIdx.y * NT;
+  const int per = (g.nkb + cs - 1) / cs;
+  const int kb0 = min(g.nkb, rank * per), nkb = min(g.nkb, kb0 + per) - kb0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Cfg::STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -87,11 +138,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(&acce[b], 4);
     }
     fence_mbar_init();
-    prefetch_tmap(&tA);
-    prefetch_tmap(&tB);
+    prefetch_tmap(&tW);
+    prefetch_tmap(&tX);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 256);
+    tmem_alloc(tmem_slot, 2 * Cfg::ACC_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -99,79 +150,143 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
-  pdl_wait();
+  if (!early_w) pdl_wait();
 
+  float2 acc[NT / 2];
+#pragma unroll
+  for (int t = 0; t < NT / 2; ++t) acc[t] = make_float2(0.f, 0.f);
   if (warp == 0) {
     if (lane == 0) {
-#pragma unroll 1
-      for (int i = 0; i < g.nkb; ++i) {
-        const int s = i % Cfg::STAGES;
-        if (!mbar_wait(&empty[s], ((uint32_t)(i / Cfg::STAGES) & 1u) ^ 1u)) break;
-        uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
-        tma_load_2d(sa, &tA, &full[s], i * kF8BK, m_tile * kF8BM);
-        if (!B_MN)
-          tma_load_2d(sa + Cfg::TILE_BYTES, &tB, &full[s], i * kF8BK, n_tile * 128);
+      // The weight does not come from the preceding grid (the quantisation of x): its first stages are under way
+      // before that grid is done.
+      auto load_w = [&](int i) {
+        uint8_t* sw = smem + i % STAGES * Cfg::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[i % STAGES], Cfg::STAGE_BYTES);
+        if (!W_MN)
+          tma_load_2d(sw, &tW, &full[i % STAGES], (kb0 + i) * kF8BK, n0);
         else
-          tma_load_2d(sa + Cfg::TILE_BYTES, &tB, &full[s], n_tile * 128, i * kF8BK);
+          tma_load_2d(sw, &tW, &full[i % STAGES], n0, (kb0 + i) * kF8BK);
+      };
+      const int ahead = early_w ? min(nkb, STAGES) : 0;
+      for (int i = 0; i < ahead; ++i) load_w(i);
+      if (early_w) pdl_wait();
+      int i = 0;
+#pragma unroll 1
+      for (; i < nkb; ++i) {
+        const int s = i % STAGES;
+        if (i >= ahead) {
+          if (!mbar_wait(&empty[s], ((uint32_t)(i / STAGES) & 1u) ^ 1u)) break;
+          load_w(i);
+        }
+        tma_load_2d(smem + s * Cfg::STAGE_BYTES + 16384, &tX, &full[s], (kb0 + i) * kF8BK, t0);
       }
+      if (i < nkb)  // a wait ran out: let the copies in flight land before the shared memory goes
+        for (int j = max(0, i - STAGES); j < i; ++j) mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, kWaitLimitNs / 16);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_fp8_f32(128, 128, g.a_e5m2 != 0, false, B_MN);
-      constexpr uint32_t b_kstep = B_MN ? 32u * 128u : 32u;
+      const uint32_t idesc = idesc_fp8_f32(128, NT, false, g.a_e5m2 != 0, false) | (W_MN ? 1u << 15 : 0u);
+      constexpr uint32_t w_kstep = W_MN ? 32u * 128u : 32u;
 #pragma unroll 1
-      for (int i = 0; i < g.nkb; ++i) {
-        const int s = i % Cfg::STAGES, b = i & 1;
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % STAGES, b = i & 1;
         if (!mbar_wait(&acce[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) break;
-        if (!mbar_wait(&full[s], (uint32_t)(i / Cfg::STAGES) & 1u)) break;
+        if (!mbar_wait(&full[s], (uint32_t)(i / STAGES) & 1u)) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + s * Cfg::STAGE_BYTES);
-        const uint32_t sb = sa + Cfg::TILE_BYTES;
+        const uint32_t sw = smem_u32(smem + s * Cfg::STAGE_BYTES);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_fp8(tmem + b * 128u, sdesc_sw128(sa + kk * 32u, 16u, 1024u), sdesc_sw128(sb + kk * b_kstep, 16u, 1024u),
-                   idesc, kk > 0 ? 1u : 0u);
+          umma_fp8(tmem + b * Cfg::ACC_COLS, sdesc_sw128(sw + kk * w_kstep, 16u, 1024u),
+                   sdesc_sw128(sw + 16384u + kk * 32u, 16u, 1024u), idesc, kk > 0 ? 1u : 0u);
         umma_commit(&empty[s]);
         umma_commit(&accf[b]);
       }
     }
   } else {
+    if (early_w) pdl_wait();
     const int q = warp & 3;
-    const int m = m_tile * kF8BM + q * 32 + lane;
-    const bool live = m < g.T;
-    float acc[128];
+    constexpr int NS = (NT + 31) / 32;
+    const float* ws = g.ws + (size_t)(n0 >> 7) * g.ws_n + (size_t)kb0 * g.ws_k;
+    // Lane l fetches the scales of tokens l, l + 32, ... one k-block ahead; every lane reads them back from the warp's
+    // own piece of shared memory, four at a time.
+    float* mine = scales + q * 2 * NT;
+    float xn[NS], wn = 0.f;
+    auto fetch = [&](int i) {
+      wn = ws[(size_t)i * g.ws_k];
 #pragma unroll
-    for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int j = 0; j < NS; ++j) {
+        const int t = t0 + 32 * j + lane;
+        xn[j] = t < g.T ? g.xs[(size_t)(kb0 + i) * g.T + t] : 0.f;
+      }
+    };
+    if (nkb > 0) fetch(0);
 #pragma unroll 1
-    for (int i = 0; i < g.nkb; ++i) {
+    for (int i = 0; i < nkb; ++i) {
       const int b = i & 1;
-      const float s = (live ? g.xs[(size_t)i * g.T + m] : 0.f) * g.ws[(size_t)n_tile * g.ws_n + (size_t)i * g.ws_k];
+      const float* sc = mine + b * NT;
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        if (NT >= 32 || lane < NT) mine[b * NT + 32 * j + lane] = xn[j] * wn;
+      __syncwarp();
+      if (i + 1 < nkb) fetch(i + 1);
       if (!mbar_wait(&accf[b], (uint32_t)(i >> 1) & 1u)) break;
       tc_fence_after();
-      const uint32_t ta = tmem + b * 128u + ((uint32_t)(q * 32) << 16);
+      const uint32_t ta = tmem + b * Cfg::ACC_COLS + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld32(ta + c * 32u, v);
+      for (int c = 0; c < NT / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld16_async(ta + c * 16, v);
+        tmem_ld_wait();
+        if (c == NT / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce[b]);
+        }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(v[j], s, acc[c * 32 + j]);
+        for (int j = 0; j < 4; ++j) {
+          const float4 s4 = *reinterpret_cast<const float4*>(sc + 16 * c + 4 * j);
+          fma2(acc[8 * c + 2 * j], v[4 * j], v[4 * j + 1], s4.x, s4.y);
+          fma2(acc[8 * c + 2 * j + 1], v[4 * j + 2], v[4 * j + 3], s4.z, s4.w);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acce[b]);
     }
-    if (live) {
+  }
+
+  // Thread (warp q, lane) of the folding warps holds weight row n0 + 32 q + lane of every token. The sums go through
+  // shared memory, [token][128] (the ring is idle: every load and MMA has been waited for), so that the splits can be
+  // added and the results leave in whole rows.
+  const int live = min(NT, g.T - t0);
+  float* sum = reinterpret_cast<float*>(smem);
+  __syncthreads();
+  if (warp >= 2) {
+    const int row = (warp & 3) * 32 + lane;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) fp8_store32(g, m, n_tile * 128 + c * 32, acc + c * 32);
+    for (int t = 0; t < NT; ++t)
+      if (t < live) sum[t * 128 + row] = (t & 1) ? acc[t / 2].y : acc[t / 2].x;
+  }
+  if (early_w) pdl_wait();
+  if (cs == 1) {
+    __syncthreads();
+    fp8_reduce_splits<1>(g, sum, 0, t0, live, n0);
+  } else {
+    cluster_sync();
+    switch (cs) {
+      case 2: fp8_reduce_splits<2>(g, sum, rank, t0, live, n0); break;
+      case 3: fp8_reduce_splits<3>(g, sum, rank, t0, live, n0); break;
+      case 4: fp8_reduce_splits<4>(g, sum, rank, t0, live, n0); break;
+      case 5: fp8_reduce_splits<5>(g, sum, rank, t0, live, n0); break;
+      case 6: fp8_reduce_splits<6>(g, sum, rank, t0, live, n0); break;
+      case 7: fp8_reduce_splits<7>(g, sum, rank, t0, live, n0); break;
+      default: fp8_reduce_splits<8>(g, sum, rank, t0, live, n0);
     }
+    cluster_sync();  // the peers have read this CTA's sums
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 2 * Cfg::ACC_COLS);
   }
 }
 
@@ -199,15 +314,6 @@ __device__ __forceinline__ void fp8_tile_coords(int t, int m_tiles, int n_tiles,
   const int rem = t % per_group;
   m = first_m + rem % gm;
   n = rem / gm;
-}
-
-// a.xy += v.xy * s (two fp32 multiply-adds in one instruction)
-__device__ __forceinline__ void fma2(float2& a, uint32_t v0, uint32_t v1, float s) {
-  asm("{\n\t.reg .b64 v, s, a;\n\t"
-      "mov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 a, {%0, %1};\n\t"
-      "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a.x), "+f"(a.y)
-      : "r"(v0), "r"(v1), "f"(s));
 }
 
 template <bool B_MN>
@@ -355,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
               if (lane == 0) mbar_arrive_cluster(done + 8 * b);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], v[2 * j], v[2 * j + 1], s);
+            for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], v[2 * j], v[2 * j + 1], s, s);
           }
         } else if (lane == 0) {
           mbar_arrive_cluster(done + 8 * b);
