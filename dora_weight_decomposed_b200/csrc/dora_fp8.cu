@@ -276,7 +276,7 @@ cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp
   const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
   const int cs = narrow_splits<NT, W_MN>(tiles * t_tiles, g.nkb);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)t_tiles);
+  cfg.gridDim = dim3((unsigned)(tiles * t_tiles * cs));
   cfg.blockDim = dim3(kF8Threads);
   cfg.dynamicSmemBytes = Fp8Narrow<NT>::SMEM_BYTES;
   cfg.stream = st;
@@ -298,8 +298,7 @@ cudaError_t launch_narrow_nt(int nt, const CUtensorMap& tw, const CUtensorMap& t
   switch (nt) {
     case 16: return launch_narrow<16, W_MN>(tw, tx, g, early_w, st);
     case 32: return launch_narrow<32, W_MN>(tw, tx, g, early_w, st);
-    case 64: return launch_narrow<64, W_MN>(tw, tx, g, early_w, st);
-    default: return launch_narrow<128, W_MN>(tw, tx, g, early_w, st);
+    default: return launch_narrow<64, W_MN>(tw, tx, g, early_w, st);
   }
 }
 
@@ -379,7 +378,7 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
   Fp8Geom g{x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
             desc->out_dtype == DORA_FP32, type == DORA_E5M2};
-  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
   const bool narrow = T <= 128;
   CUtensorMap tx, tw;
   cudaError_t e = make_map_u8(&tx, x, T, K, narrow ? nt : 128);

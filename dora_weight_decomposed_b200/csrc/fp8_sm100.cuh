@@ -63,7 +63,8 @@ __device__ __forceinline__ void fma2(float2& a, uint32_t v0, uint32_t v1, float 
 // ------------------------------------------------------------------ few tokens
 //
 // With few tokens the weight's bytes are the cost, so the operands change places: 128 rows of the weight are the
-// MMA's M, the NT tokens its N, and D holds the result transposed (lane = weight row, column = token). The K
+// MMA's M, NT tokens its N (64 at most: T = 128 of 8192 x 8192 takes 28.9 us in two tiles of 64 tokens and 33.5 in
+// one of 128, whose folding is the longer chain), and D holds the result transposed (lane = weight row, column = token). The K
 // blocks of a tile are split over the CTAs of a cluster so that enough of the weight is in flight on every SM; two
 // CTAs fit on one SM. Each CTA folds its k-blocks into registers; the cluster then adds the splits
 // through distributed shared memory in rank order, so the result does not depend on timing.
@@ -72,7 +73,7 @@ template <int NT>
 struct Fp8Narrow {
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = 16384 + X_BYTES;
-  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4;
   static constexpr int SCALE_BYTES = 4 * 2 * NT * 4;  // per folding warp: two k-blocks' token scales
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES + 256 + 1024;
   static constexpr uint32_t ACC_COLS = NT < 32 ? 16 : NT;  // two accumulators; TMEM comes in 32 columns at least
@@ -124,7 +125,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = blockIdx.x % cs;  // the cluster's CTAs are neighbours in x
-  const int n0 = blockIdx.x / cs * 128, t0 = blockIdx.y * NT;
+  const int t_tiles = (g.T + NT - 1) / NT;  // the token tiles of a weight tile run side by side and share it in L2
+  const int n0 = blockIdx.x / cs / t_tiles * 128, t0 = blockIdx.x / cs % t_tiles * NT;
   const int per = (g.nkb + cs - 1) / cs;
   const int kb0 = min(g.nkb, rank * per), nkb = min(g.nkb, kb0 + per) - kb0;
 
