@@ -77,27 +77,48 @@ static_assert(sizeof(AdamTable) < 32600, "kernel parameters");
 
 // ------------------------------------------------------------------ loads and stores of 8 elements
 
-// Elements i .. i + 7 of an n-element tensor as fp32, zeros beyond it; vec: the base is 16-byte aligned.
-__device__ __forceinline__ void load8(const void* base, int fp32, int vec, int64_t i, int64_t n, float* v) {
+// Elements i .. i + 7 as they lie in memory: bf16 in a, fp32 in a and b; zeros beyond the tensor.
+struct Raw8 {
+  uint4 a, b;
+};
+
+// vec: the base is 16-byte aligned.
+__device__ __forceinline__ Raw8 load_raw(const void* base, int fp32, int vec, int64_t i, int64_t n) {
+  Raw8 r;
+  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
   if (vec && i + 8 <= n) {
-    if (fp32) {
-      const float4* p = reinterpret_cast<const float4*>((const float*)base + i);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)base + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)base + i * (fp32 ? 4 : 2));
+    r.a = p[0];
+    if (fp32) r.b = p[1];
+  } else if (i < n) {
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+    for (int j = 0; j < 8; ++j) {
+      if (i + j >= n) continue;
+      if (fp32)
+        w[j] = ((const uint32_t*)base)[i + j];
+      else
+        w[j / 2] |= (uint32_t)((const uint16_t*)base)[i + j] << (16 * (j & 1));
     }
-    return;
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    r.b = make_uint4(w[4], w[5], w[6], w[7]);
   }
+  return r;
+}
+
+__device__ __forceinline__ void values(const Raw8& r, int fp32, float* v) {
+  if (fp32) {
+    v[0] = __uint_as_float(r.a.x), v[1] = __uint_as_float(r.a.y), v[2] = __uint_as_float(r.a.z);
+    v[3] = __uint_as_float(r.a.w), v[4] = __uint_as_float(r.b.x), v[5] = __uint_as_float(r.b.y);
+    v[6] = __uint_as_float(r.b.z), v[7] = __uint_as_float(r.b.w);
+  } else {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = i + j >= n ? 0.f : fp32 ? ((const float*)base)[i + j] : __bfloat162float(((const __nv_bfloat16*)base)[i + j]);
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
 }
 
 __device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i, int64_t n, const float* v) {
@@ -125,7 +146,7 @@ __device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i,
 }
 
 // 8 e4m3 codes (zeros beyond n).
-__device__ __forceinline__ void load8_codes(const uint8_t* base, int64_t i, int64_t n, float* v) {
+__device__ __forceinline__ uint2 load_codes(const uint8_t* base, int64_t i, int64_t n) {
   uint2 u = make_uint2(0u, 0u);
   if (i + 8 <= n) {
     u = *reinterpret_cast<const uint2*>(base + i);
@@ -134,28 +155,39 @@ __device__ __forceinline__ void load8_codes(const uint8_t* base, int64_t i, int6
     for (int j = 0; j < 8; ++j)
       if (i + j < n) (j < 4 ? u.x : u.y) |= (uint32_t)base[i + j] << (8 * (j & 3));
   }
+  return u;
+}
+
+__device__ __forceinline__ void code_values(uint2 u, float* v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint16_t two = (uint16_t)((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    const __half2 hh = *reinterpret_cast<const __half2*>(&h);
-    const float2 f = __half22float2(hh);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     v[2 * j] = f.x;
     v[2 * j + 1] = f.y;
   }
 }
 
-__device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, const uint32_t* code) {
-  const uint2 u = make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                             code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+__device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, int64_t n, uint2 u) {
   if (i + 8 <= n) {
     *reinterpret_cast<uint2*>(base + i) = u;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j < n) base[i + j] = (uint8_t)code[j];
+      if (i + j < n) base[i + j] = (uint8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
   }
+}
+
+// The chunks [first, last) of one CTA: contiguous, so that the tensor they lie in is found once and then followed.
+struct Range {
+  int first, last;
+};
+__device__ __forceinline__ Range cta_range(int chunks) {
+  const int per = chunks / (int)gridDim.x, more = chunks % (int)gridDim.x, b = blockIdx.x;
+  const int first = b * per + min(b, more);
+  return {first, first + per + (b < more ? 1 : 0)};
 }
 
 // ------------------------------------------------------------------ gradient norm
@@ -170,13 +202,16 @@ __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __gri
   pdl_trigger();
   pdl_wait();
   double sum = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int k = find_tensor(t, c);
+  const Range range = cta_range(t.chunks);
+  int k = find_tensor(t, range.first);
+#pragma unroll 4
+  for (int c = range.first; c < range.last; ++c) {
+    while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
     const GradEntry& e = t.e[k];
     const int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
     if (i >= e.n) continue;
     float v[8];
-    load8(e.g, e.fp32, e.vec, i, e.n, v);
+    values(load_raw(e.g, e.fp32, e.vec, i, e.n), e.fp32, v);
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
@@ -236,16 +271,17 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// |y| <= 448 as an e4m3 code: floor(|y| / step + u / 65536), step being the code spacing at |y|. Above 2^-6 the
-// spacing is 2^-3 of the binade, so the code is the top bits of the fp32 pattern after u is added below them; under
-// 2^-6 it is 2^-9 throughout, and adding 2^-6 brings the same bits into the same place.
-__device__ __forceinline__ uint32_t stochastic_code(float y, uint32_t u) {
-  const bool low = fabsf(y) < 0.015625f;
-  const float a = fabsf(y) + (low ? 0.015625f : 0.f);
-  return ((__float_as_uint(a) + (u << 4)) >> 20) - (low ? 121u << 3 : 120u << 3);
+// |y| <= 448 as an e4m3 code: floor(|y| / step + u / 65536), step being the code spacing at |y|. From 2^-6 up the
+// spacing is 2^-3 of the binade, so the code is the top bits of the fp32 pattern (exponent offset 120) after u is
+// added below them. Under 2^-6 it is 2^-9 throughout, and adding 2^-6 brings the same bits into the same place
+// (offset 121). Each of the two is the larger one where it holds.
+__device__ __forceinline__ uint32_t stochastic_code(float y, uint32_t u16) {
+  const float a = fabsf(y);
+  const int t = max(__float_as_int(a) - (120 << 23), __float_as_int(a + 0.015625f) - (121 << 23));
+  return (uint32_t)(t + (int)u16) >> 20;  // u16 = 16 u
 }
 
-// The scale of a block of 16 lanes x 8 moments (all warps' lanes take part), and y = v / scale.
+// The scale of a block of 16 lanes x 8 moments (all of the warp's lanes take part); not finite if one of them is not.
 __device__ __forceinline__ float moment_scale(const float* v) {
   float amax = 0.f;
 #pragma unroll
@@ -260,77 +296,148 @@ __device__ __forceinline__ float moment_scale(const float* v) {
   return s;
 }
 
+// a / b rounded to nearest from the rounded reciprocal of b (Markstein's quotient step).
+__device__ __forceinline__ float quotient(float a, float b, float inv_b) {
+  const float q = a * inv_b;
+  return fmaf(fmaf(-q, b, a), inv_b, q);
+}
+
+// What a thread reads of a chunk: its eight elements of everything.
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable t, const AdamArgs a,
-                                                         dora_adamw_control_t* __restrict__ control,
-                                                         const float* __restrict__ grad_scale, int last) {
+struct Elements {
+  Raw8 g, p, m, v;  // m, v: 32 bits
+  uint2 cm, cv;     // 8 bits
+  float sm, sv;
+  int k;
+  int64_t i;
+};
+
+template <int BITS>
+__device__ __forceinline__ void fetch(const AdamTable& t, int c, int k, Elements<BITS>& x) {
+  while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
+  const AdamEntry& e = t.e[k];
+  const int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
+  x.k = k;
+  x.i = i;
+  x.g = load_raw(e.g, e.g_fp32, e.g_vec, i, e.n);
+  x.p = e.master ? load_raw(e.master, 1, 1, i, e.n) : load_raw(e.p, e.p_fp32, e.p_vec, i, e.n);
+  if (BITS == 32) {
+    x.m = load_raw(e.avg, 1, 1, i, e.n);
+    x.v = load_raw(e.sq, 1, 1, i, e.n);
+  } else {
+    x.cm = load_codes((const uint8_t*)e.avg, i, e.n);
+    x.cv = load_codes((const uint8_t*)e.sq, i, e.n);
+    x.sm = i < e.n ? e.savg[i >> 7] : 0.f;
+    x.sv = i < e.n ? e.ssq[i >> 7] : 0.f;
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ void update(const AdamTable& t, const AdamArgs& a, const Elements<BITS>& x, float gs, float lr,
+                                       float lr1, float rbc2, uint32_t key) {
+  const AdamEntry& e = t.e[x.k];
+  const int64_t i = x.i, n = e.n;
+  float g[8], p[8], m[8], v[8], r[8];
+  values(x.g, e.g_fp32, g);
+  values(x.p, e.master || e.p_fp32, p);
+  if (BITS == 32) {
+    values(x.m, 1, m);
+    values(x.v, 1, v);
+  } else {
+    code_values(x.cm, m);
+    code_values(x.cv, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] *= x.sm;
+      v[j] *= x.sv;
+      v[j] *= v[j];
+    }
+  }
+  const float keep = 1.0f - lr * e.wd;
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // Each product and sum rounded by itself: the moments' stored codes then depend on the formula alone.
+    const float gj = __fmul_rn(g[j], gs);
+    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.omb1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.omb2));
+    top = fmaxf(top, v[j]);
+  }
+  if (top < 1e37f) {
+    // sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2 (to the last place); zero for v = 0.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float y;
+      asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v[j], 1e-37f)));
+      const float s = v[j] * y;
+      r[j] = fmaf(fmaf(-s, s, v[j]), 0.5f * y, s);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = sqrtf(v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) p[j] = p[j] * keep - __fdividef(m[j] * lr1, fmaf(r[j], rbc2, a.eps));
+  if (e.master) store8(e.master, 1, 1, i, n, p);
+  store8(e.p, e.p_fp32, e.p_vec, i, n, p);
+  if (BITS == 32) {
+    store8(e.avg, 1, 1, i, n, m);
+    store8(e.sq, 1, 1, i, n, v);
+    return;
+  }
+  const float sm = moment_scale(m), sr = moment_scale(r);
+  uint2 cm = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), cr = cm;  // NaN codes
+  if (sm < 1e38f && sr < 1e38f) {
+    const float im = 1.0f / sm, ir = 1.0f / sr;
+    uint32_t wm[2] = {0, 0}, wr[2] = {0, 0};
+    const uint32_t pair0 = e.index0 + (uint32_t)(i >> 1);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t h = mix((pair0 + j / 2) ^ key);
+      const uint32_t u[2] = {h << 4 & 0xffff0u, h >> 12 & 0xffff0u};
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const float ym = quotient(m[j + d], sm, im), yr = quotient(r[j + d], sr, ir);
+        const uint32_t km = stochastic_code(ym, u[d]) | (__float_as_uint(ym) >> 24 & 0x80u);
+        const uint32_t kr = max(stochastic_code(yr, u[d]), r[j + d] > 0.f ? 1u : 0u);
+        wm[j / 4] |= km << (8 * (j % 4 + d));
+        wr[j / 4] |= kr << (8 * (j % 4 + d));
+      }
+    }
+    cm = make_uint2(wm[0], wm[1]);
+    cr = make_uint2(wr[0], wr[1]);
+  }
+  store_codes((uint8_t*)e.avg, i, n, cm);
+  store_codes((uint8_t*)e.sq, i, n, cr);
+  if ((threadIdx.x & 15) == 0 && i < n) {
+    e.savg[i >> 7] = sm;
+    e.ssq[i >> 7] = sr;
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamTable t, const AdamArgs a,
+                                                            dora_adamw_control_t* __restrict__ control,
+                                                            const float* __restrict__ grad_scale, int last) {
   pdl_trigger();
   pdl_wait();
   const int64_t step = control->step + 1;
   const float lr = control->lr;
   const float gs = grad_scale ? *grad_scale : 1.0f;
   const bool run = isfinite(gs);
-  const float bc1 = -expm1f((float)step * a.ln_b1), bc2 = -expm1f((float)step * a.ln_b2);
-  const float lr1 = lr / bc1, rbc2 = 1.0f / sqrtf(bc2);
-  const uint32_t key = mix(a.seed + (uint32_t)step * 0x9E3779B9u);
-  for (int c = blockIdx.x; run && c < t.chunks; c += gridDim.x) {
-    const int k = find_tensor(t, c);
-    const AdamEntry& e = t.e[k];
-    const int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
-    const int64_t n = e.n;
-    float g[8], p[8], m[8], v[8], r[8];
-    load8(e.g, e.g_fp32, e.g_vec, i, n, g);
-    if (e.master)
-      load8(e.master, 1, 1, i, n, p);
-    else
-      load8(e.p, e.p_fp32, e.p_vec, i, n, p);
-    if (BITS == 32) {
-      load8(e.avg, 1, 1, i, n, m);
-      load8(e.sq, 1, 1, i, n, v);
-    } else {
-      const int64_t blk = i >> 7;
-      const float sm = i < n ? e.savg[blk] : 0.f, sr = i < n ? e.ssq[blk] : 0.f;
-      load8_codes((const uint8_t*)e.avg, i, n, m);
-      load8_codes((const uint8_t*)e.sq, i, n, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] *= sm;
-        v[j] *= sr;
-        v[j] *= v[j];
-      }
-    }
-    const float keep = 1.0f - lr * e.wd;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // Each product and sum rounded by itself: the moments' stored codes then depend on the formula alone.
-      const float gj = __fmul_rn(g[j], gs);
-      m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.omb1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.omb2));
-      r[j] = sqrtf(v[j]);
-      p[j] = p[j] * keep - __fdividef(m[j] * lr1, fmaf(r[j], rbc2, a.eps));
-    }
-    if (e.master) store8(e.master, 1, 1, i, n, p);
-    store8(e.p, e.p_fp32, e.p_vec, i, n, p);
-    if (BITS == 32) {
-      store8(e.avg, 1, 1, i, n, m);
-      store8(e.sq, 1, 1, i, n, v);
-    } else {
-      const float sm = moment_scale(m), sr = moment_scale(r);
-      uint32_t cm[8], cr[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t h = mix((e.index0 + (uint32_t)((i + j) >> 1)) ^ key);
-        const uint32_t u = (j & 1) ? h >> 16 : h & 0xffffu;
-        const float ym = m[j] / sm, yr = r[j] / sr;
-        cm[j] = isnan(ym) ? 0x7fu : stochastic_code(ym, u) | (__float_as_uint(ym) >> 31 << 7);
-        cr[j] = isnan(yr) ? 0x7fu : max(stochastic_code(yr, u), yr > 0.f ? 1u : 0u);
-      }
-      store8_codes((uint8_t*)e.avg, i, n, cm);
-      store8_codes((uint8_t*)e.sq, i, n, cr);
-      if ((threadIdx.x & 15) == 0 && i < n) {
-        e.savg[i >> 7] = sm;
-        e.ssq[i >> 7] = sr;
-      }
+  const Range range = cta_range(t.chunks);
+  if (run && range.first < range.last) {
+    // The next chunk's loads are under way while this one is computed.
+    Elements<BITS> now, next;
+    fetch<BITS>(t, range.first, find_tensor(t, range.first), now);
+    const float bc1 = -expm1f((float)step * a.ln_b1), bc2 = -expm1f((float)step * a.ln_b2);
+    const float lr1 = lr / bc1, rbc2 = 1.0f / sqrtf(bc2);
+    const uint32_t key = mix(a.seed + (uint32_t)step * 0x9E3779B9u);
+#pragma unroll 1
+    for (int c = range.first; c < range.last; ++c) {
+      if (c + 1 < range.last) fetch<BITS>(t, c + 1, now.k, next);
+      update<BITS>(t, a, now, gs, lr, lr1, rbc2, key);
+      now = next;
     }
   }
   // The last CTA of the call's last launch counts the step: by then every CTA has read the count.
@@ -450,7 +557,7 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
   const AdamArgs a{(float)desc->beta1,          (float)(1.0 - desc->beta1),   (float)desc->beta2,
                    (float)(1.0 - desc->beta2),  (float)std::log(desc->beta1), (float)std::log(desc->beta2),
                    desc->eps,                   desc->seed};
-  const int most = device_sm_count() * 4;
+  const int most = device_sm_count() * 3;
   cudaError_t e = cudaSuccess;
   AdamTable t;
   int i = 0;

@@ -199,15 +199,19 @@ cudaError_t quantize(int64_t rows, int64_t cols, dora_dtype_t in, dora_dtype_t f
 
 // ------------------------------------------------------------------ products
 
-// Row-major 8-bit matrix [rows x cols] in boxes of box_rows x 128 columns, 128-byte swizzle, zeros out of bounds.
-cudaError_t make_map_u8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_rows) {
+// Row-major matrix [rows x cols] of elements of `size` bytes in boxes of box_rows x 128 bytes, 128-byte swizzle, zeros
+// out of bounds.
+cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int size, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols};
-  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * size};
+  cuuint32_t box[2] = {128u / size, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1u, 1u};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  const CUtensorMapDataType type = size == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = enc(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -304,13 +308,22 @@ cudaError_t launch_narrow_nt(int nt, const CUtensorMap& tw, const CUtensorMap& t
 
 template <bool B_MN>
 cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Geom& g, cudaStream_t st) {
+  CUtensorMap tout;
+  cudaError_t e = make_map_2d(&tout, g.out, g.T, g.N, g.out_fp32 ? 4 : 2, 32);
+  if (e != cudaSuccess) return e;
   auto kern = fp8_pair_kernel<B_MN>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, kern, kF8PairSmem);
+  e = set_smem_once(smem_set, kern, kF8PairSmem);
   if (e != cudaSuccess) return e;
+  // The register moves in the kernel count on this many registers per thread at launch.
+  static const int regs = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs < kF8LaunchRegs) return cudaErrorInvalidKernelImage;
   const int64_t pairs = std::min<int64_t>(cdiv(g.T, 256) * cdiv(g.N, 256), std::max(1, device_sm_count() / 2));
   ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
-  return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, g);
+  return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, tout, g);
 }
 
 // What a call keeps in its workspace: the quantised operand and its scales.
@@ -381,8 +394,8 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
   const bool narrow = T <= 128;
   CUtensorMap tx, tw;
-  cudaError_t e = make_map_u8(&tx, x, T, K, narrow ? nt : 128);
-  if (e == cudaSuccess) e = make_map_u8(&tw, W, desc->d_out, desc->d_in, 128);
+  cudaError_t e = make_map_2d(&tx, x, T, K, 1, narrow ? nt : 128);
+  if (e == cudaSuccess) e = make_map_2d(&tw, W, desc->d_out, desc->d_in, 1, 128);
   if (e == cudaSuccess) {
     if (narrow)
       e = backward ? launch_narrow_nt<true>(nt, tw, tx, g, !given, st) : launch_narrow_nt<false>(nt, tw, tx, g, !given, st);

@@ -26,28 +26,10 @@ struct Fp8Geom {
   int a_e5m2;
 };
 
-// 32 results of one row, columns n .. n + 31 (N is a multiple of 16).
-__device__ __forceinline__ void fp8_store32(const Fp8Geom& g, int m, int n, const float* v) {
+// Eight 16-byte pieces of one row of a box (32 rows of 128 bytes, 128-byte swizzle), as a tiled store reads it.
+__device__ __forceinline__ void fp8_stage_row(uint8_t* box, int lane, const uint4 (&p)[8]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (n + 16 * h >= g.N) return;
-    const size_t at = (size_t)m * g.N + n + 16 * h;
-    if (g.out_fp32) {
-      float4* o = reinterpret_cast<float4*>((float*)g.out + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = make_float4(v[16 * h + 4 * i], v[16 * h + 4 * i + 1], v[16 * h + 4 * i + 2], v[16 * h + 4 * i + 3]);
-    } else {
-      uint4* o = reinterpret_cast<uint4*>((__nv_bfloat16*)g.out + at);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        __nv_bfloat162 p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = __floats2bfloat162_rn(v[16 * h + 8 * i + 2 * j], v[16 * h + 8 * i + 2 * j + 1]);
-        o[i] = *reinterpret_cast<const uint4*>(p);
-      }
-    }
-  }
+  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = p[i];
 }
 
 // a.xy += v.xy * s.xy: two fp32 multiply-adds in one instruction (T = 512, K = 16384 on 16 pairs: 71 us, 84 us with
@@ -303,10 +285,16 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 // about half as many instructions as a k-block of MMAs takes clocks. Tiles
 // are walked persistently; the MMAs of the next tile start while this one is stored.
 constexpr int kF8FoldWarps = 8;
-constexpr int kF8PairThreads = 64 + 32 * kF8FoldWarps;
+constexpr int kF8PairThreads = 128 + 32 * kF8FoldWarps;
+// The block launches with 384 x 168 registers, the most that 384 threads can have; the folding warps take 216 each and
+// leave 72 to the others: 256 * 216 + 128 * 72 = 384 * 168. (With 168 for all, the sums spill.)
+constexpr int kF8LaunchRegs = 168, kF8FoldRegs = 216, kF8OtherRegs = 72;
+static_assert(32 * kF8FoldWarps * kF8FoldRegs + 128 * kF8OtherRegs <= kF8PairThreads * kF8LaunchRegs, "registers");
 constexpr int kF8PairStages = 6;
 constexpr int kF8StageBytes = 2 * 128 * 128;
-constexpr int kF8PairSmem = kF8PairStages * kF8StageBytes + 256 + 1024;
+constexpr int kF8OutBytes = 4096;  // one box of results per folding warp: 32 rows of 128 bytes
+constexpr int kF8PairSmem = kF8PairStages * kF8StageBytes + kF8FoldWarps * kF8OutBytes + 256 + 1024;
+static_assert(kF8PairSmem <= 227 * 1024, "shared memory");
 
 // Tiles in groups of 8 rows of tiles, rows fastest: the tiles in flight share operands in L2.
 __device__ __forceinline__ void fp8_tile_coords(int t, int m_tiles, int n_tiles, int& m, int& n) {
@@ -320,11 +308,13 @@ __device__ __forceinline__ void fp8_tile_coords(int t, int m_tiles, int n_tiles,
 
 template <bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB, const Fp8Geom g) {
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
+                    const __grid_constant__ CUtensorMap tOut, const Fp8Geom g) {
   constexpr int STAGES = kF8PairStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * kF8StageBytes);  // used in the leader
+  uint8_t* out_smem = smem + STAGES * kF8StageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_smem + kF8FoldWarps * kF8OutBytes);  // used in the leader
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;  // [2] accumulator complete
   uint64_t* acce = accf + 2;        // [2] accumulator folded by both CTAs, used in the leader
@@ -349,6 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&tA);
     prefetch_tmap(&tB);
+    prefetch_tmap(&tOut);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -362,7 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  if (warp < 2) {
+  if (warp < 4) {
+    setmaxnreg_dec<kF8OtherRegs>();
     if (warp == 0 && lane == 0) {
       int it = 0;
       bool ok = true;
@@ -418,8 +410,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
       }
     }
   } else {
+    setmaxnreg_inc<kF8FoldRegs>();
     constexpr int COLS = 4 * 256 / kF8FoldWarps;  // columns per warp
-    const int q = warp & 3, part = (warp - 2) >> 2;
+    const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t done = mapa_shared(smem_u32(acce), 0);
     int it = 0;
     bool ok = true;
@@ -469,11 +462,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
           mbar_arrive_cluster(done + 8 * b);
         }
       }
-      if (ok && live && m < g.T) {
+      // Results leave by tiled stores of 32 rows x 128 bytes from one box per warp, so that the next tile's folding
+      // begins after a few hundred clocks (row-per-thread stores: 3.2 us a tile; what lies outside is dropped).
+      if (ok && live) {
+        uint8_t* box = out_smem + (warp - 4) * kF8OutBytes;
+        auto send = [&](int c, int n, const uint4 (&p)[8]) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          fp8_stage_row(box, lane, p);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n < g.N) tma_store_2d(&tOut, box, n, mw);
+            bulk_commit();
+          }
+        };
+        if (g.out_fp32) {
 #pragma unroll
-        for (int c = 0; c < COLS / 32; ++c) fp8_store32(g, m, n0 + c * 32, reinterpret_cast<const float*>(acc) + c * 32);
+          for (int c = 0; c < COLS / 32; ++c) {
+            uint4 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              p[i] = make_uint4(__float_as_uint(acc[16 * c + 2 * i].x), __float_as_uint(acc[16 * c + 2 * i].y),
+                                __float_as_uint(acc[16 * c + 2 * i + 1].x), __float_as_uint(acc[16 * c + 2 * i + 1].y));
+            send(c, n0 + 32 * c, p);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < COLS / 64; ++c) {
+            uint4 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              __nv_bfloat162 h[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(acc[32 * c + 4 * i + j]);
+              p[i] = *reinterpret_cast<const uint4*>(h);
+            }
+            send(c, n0 + 64 * c, p);
+          }
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
