@@ -69,11 +69,42 @@ struct AdamEntry {
   int64_t n;
   uint32_t index0;  // of pairs: (index0 + i) / 2 modulo 2^32
   float wd;
-  int p_fp32, g_fp32, p_vec, g_vec;
+  uint8_t p_fp32, g_fp32, p_vec, g_vec;
 };
-constexpr int kMaxAdam = 340;
+constexpr int kMaxAdam = 385;
 using AdamTable = Table<AdamEntry, kMaxAdam>;
 static_assert(sizeof(AdamTable) < 32600, "kernel parameters");
+
+// ------------------------------------------------------------------ two fp32 at a time
+
+// The 8-bit step is bound by its instructions, so its arithmetic is done on pairs (one instruction for two, each
+// rounded by itself).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 r, a, b;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 r, a, b;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
 // ------------------------------------------------------------------ loads and stores of 8 elements
 
@@ -106,31 +137,29 @@ __device__ __forceinline__ Raw8 load_raw(const void* base, int fp32, int vec, in
   return r;
 }
 
-__device__ __forceinline__ void values(const Raw8& r, int fp32, float* v) {
+__device__ __forceinline__ void values(const Raw8& r, int fp32, float2 (&v)[4]) {
   if (fp32) {
-    v[0] = __uint_as_float(r.a.x), v[1] = __uint_as_float(r.a.y), v[2] = __uint_as_float(r.a.z);
-    v[3] = __uint_as_float(r.a.w), v[4] = __uint_as_float(r.b.x), v[5] = __uint_as_float(r.b.y);
-    v[6] = __uint_as_float(r.b.z), v[7] = __uint_as_float(r.b.w);
+    v[0] = make_float2(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+    v[1] = make_float2(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+    v[2] = make_float2(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+    v[3] = make_float2(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
   } else {
     const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   }
 }
 
-__device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i, int64_t n, const float* v) {
+__device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i, int64_t n, const float2 (&v)[4]) {
   if (vec && i + 8 <= n) {
     if (fp32) {
       float4* p = reinterpret_cast<float4*>((float*)base + i);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
       __nv_bfloat162 h[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(v[j]);
       *reinterpret_cast<uint4*>((__nv_bfloat16*)base + i) = *reinterpret_cast<const uint4*>(h);
     }
     return;
@@ -138,10 +167,11 @@ __device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i,
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (i + j >= n) return;
+    const float x = (j & 1) ? v[j / 2].y : v[j / 2].x;
     if (fp32)
-      ((float*)base)[i + j] = v[j];
+      ((float*)base)[i + j] = x;
     else
-      ((__nv_bfloat16*)base)[i + j] = __float2bfloat16_rn(v[j]);
+      ((__nv_bfloat16*)base)[i + j] = __float2bfloat16_rn(x);
   }
 }
 
@@ -158,15 +188,13 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* base, int64_t i, int6
   return u;
 }
 
-__device__ __forceinline__ void code_values(uint2 u, float* v) {
+__device__ __forceinline__ void code_values(uint2 u, float2 (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint16_t two = (uint16_t)((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[2 * j] = f.x;
-    v[2 * j + 1] = f.y;
+    v[j] = __half22float2(*reinterpret_cast<const __half2*>(&h));
   }
 }
 
@@ -195,6 +223,21 @@ __device__ __forceinline__ Range cta_range(int chunks) {
 constexpr int kNormBlocksPerSM = 4;
 constexpr int kNormBlocksMax = 1024;
 
+// Sum of eight squares, in fp32 where it holds them.
+__device__ __forceinline__ double squares(const Raw8& raw, int fp32) {
+  float2 v[4];
+  values(raw, fp32, v);
+  float2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) s = fma2(v[j], v[j], s);
+  const float a = s.x + s.y;
+  if (a > 1e-30f && a < 1e38f) return (double)a;
+  double d = 0.0;  // squares beyond the range of fp32 (or zeros, or not finite)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d += (double)v[j].x * v[j].x + (double)v[j].y * v[j].y;
+  return d;
+}
+
 // Sum of squares of this CTA's chunks: 8 values in fp32, everything above in double.
 __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __grid_constant__ GradTable t,
                                                                      double* __restrict__ part) {
@@ -203,24 +246,19 @@ __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __gri
   pdl_wait();
   double sum = 0.0;
   const Range range = cta_range(t.chunks);
-  int k = find_tensor(t, range.first);
-#pragma unroll 4
-  for (int c = range.first; c < range.last; ++c) {
-    while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
+  for (int c = range.first, k = find_tensor(t, range.first); c < range.last; ++k) {
+    // This CTA's chunks of tensor k, four loads in flight per thread.
     const GradEntry& e = t.e[k];
-    const int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
-    if (i >= e.n) continue;
-    float v[8];
-    values(load_raw(e.g, e.fp32, e.vec, i, e.n), e.fp32, v);
-    float s = 0.f;
+    const int end = min(range.last, k + 1 < t.n ? t.first[k + 1] : t.chunks);
+    int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
+    for (; c < end; c += 4, i += 4 * kChunk) {
+      Raw8 raw[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
-    if (s > 1e-30f && s < 1e38f) {
-      sum += (double)s;
-    } else {  // squares that fp32 cannot hold (or zeros, or not finite)
+      for (int j = 0; j < 4; ++j) raw[j] = load_raw(e.g, e.fp32, e.vec, i + j * kChunk, c + j < end ? e.n : 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
+      for (int j = 0; j < 4; ++j) sum += squares(raw[j], e.fp32);
     }
+    c = end;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -271,21 +309,25 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// |y| <= 448 as an e4m3 code: floor(|y| / step + u / 65536), step being the code spacing at |y|. From 2^-6 up the
-// spacing is 2^-3 of the binade, so the code is the top bits of the fp32 pattern (exponent offset 120) after u is
-// added below them. Under 2^-6 it is 2^-9 throughout, and adding 2^-6 brings the same bits into the same place
-// (offset 121). Each of the two is the larger one where it holds.
-__device__ __forceinline__ uint32_t stochastic_code(float y, uint32_t u16) {
-  const float a = fabsf(y);
-  const int t = max(__float_as_int(a) - (120 << 23), __float_as_int(a + 0.015625f) - (121 << 23));
-  return (uint32_t)(t + (int)u16) >> 20;  // u16 = 16 u
+// 0 <= y <= 448 as an e4m3 code, floor(y / step + u / 65536) with step the code spacing at y, in the top byte of the
+// result (below its top bit). From 2^-6 up the spacing is 2^-3 of the binade, so the code is the top bits of the fp32
+// pattern (exponent offset 120) after u is added below them. Under 2^-6 it is 2^-9 throughout, and adding 2^-6 brings
+// the same bits into the same place (offset 121). Doubling y moves the first offset to 121 too, and the larger of
+// the two is the one that holds. least: 2^-6 (1 + k / 8) makes it code k at least. u16 = 16 u.
+// twice = 2 y, low = y + 2^-6.
+__device__ __forceinline__ uint32_t stochastic_code(float twice, float low, uint32_t u16, float least) {
+  const float t = fmaxf(fmaxf(twice, low), least);
+  return (__float_as_uint(t) + u16 - (121u << 23)) << 4;
 }
 
 // The scale of a block of 16 lanes x 8 moments (all of the warp's lanes take part); not finite if one of them is not.
-__device__ __forceinline__ float moment_scale(const float* v) {
+__device__ __forceinline__ float moment_scale(const float2 (&v)[4]) {
   float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(v[j])));
+  for (int j = 0; j < 4; ++j) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(v[j].x)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(v[j].y)));
+  }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     const float b = __shfl_xor_sync(0xffffffffu, amax, o);
@@ -297,87 +339,98 @@ __device__ __forceinline__ float moment_scale(const float* v) {
 }
 
 // a / b rounded to nearest from the rounded reciprocal of b (Markstein's quotient step).
-__device__ __forceinline__ float quotient(float a, float b, float inv_b) {
-  const float q = a * inv_b;
-  return fmaf(fmaf(-q, b, a), inv_b, q);
+__device__ __forceinline__ float2 quotient(float2 a, float b, float inv_b) {
+  const float2 q = mul2(a, both(inv_b));
+  return fma2(fma2(neg2(q), both(b), a), both(inv_b), q);
 }
 
-// What a thread reads of a chunk: its eight elements of everything.
-template <int BITS>
-struct Elements {
-  Raw8 g, p, m, v;  // m, v: 32 bits
-  uint2 cm, cv;     // 8 bits
-  float sm, sv;
-  int k;
-  int64_t i;
+// sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2 (to the last place); zero for v = 0, NaN for inf.
+__device__ __forceinline__ float2 root(float2 v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1e-37f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1e-37f)));
+  const float2 s = mul2(v, y);
+  return fma2(fma2(neg2(s), s, v), mul2(y, both(0.5f)), s);
+}
+
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// 1 / b for a normal b: the approximation with one Newton step.
+__device__ __forceinline__ float inverse(float b) {
+  const float r = reciprocal(b);
+  return fmaf(fmaf(-b, r, 1.0f), r, r);
+}
+
+// The four top bytes, first in the lowest place.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+struct StepScalars {
+  float gs, lr, lr1, rbc2;
+  uint32_t key;
 };
 
+// Eight elements (i .. i + 7 of tensor e) of one thread.
 template <int BITS>
-__device__ __forceinline__ void fetch(const AdamTable& t, int c, int k, Elements<BITS>& x) {
-  while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
-  const AdamEntry& e = t.e[k];
-  const int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
-  x.k = k;
-  x.i = i;
-  x.g = load_raw(e.g, e.g_fp32, e.g_vec, i, e.n);
-  x.p = e.master ? load_raw(e.master, 1, 1, i, e.n) : load_raw(e.p, e.p_fp32, e.p_vec, i, e.n);
-  if (BITS == 32) {
-    x.m = load_raw(e.avg, 1, 1, i, e.n);
-    x.v = load_raw(e.sq, 1, 1, i, e.n);
-  } else {
-    x.cm = load_codes((const uint8_t*)e.avg, i, e.n);
-    x.cv = load_codes((const uint8_t*)e.sq, i, e.n);
-    x.sm = i < e.n ? e.savg[i >> 7] : 0.f;
-    x.sv = i < e.n ? e.ssq[i >> 7] : 0.f;
-  }
-}
-
-template <int BITS>
-__device__ __forceinline__ void update(const AdamTable& t, const AdamArgs& a, const Elements<BITS>& x, float gs, float lr,
-                                       float lr1, float rbc2, uint32_t key) {
-  const AdamEntry& e = t.e[x.k];
-  const int64_t i = x.i, n = e.n;
-  float g[8], p[8], m[8], v[8], r[8];
-  values(x.g, e.g_fp32, g);
-  values(x.p, e.master || e.p_fp32, p);
-  if (BITS == 32) {
-    values(x.m, 1, m);
-    values(x.v, 1, v);
-  } else {
-    code_values(x.cm, m);
-    code_values(x.cv, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] *= x.sm;
-      v[j] *= x.sv;
-      v[j] *= v[j];
+__device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, const StepScalars& c, int64_t i) {
+  const int64_t n = e.n;
+  float2 g[4], p[4], m[4], v[4], r[4];
+  float sm = 0.f, sr = 0.f;
+  {
+    const Raw8 rg = load_raw(e.g, e.g_fp32, e.g_vec, i, n);
+    const Raw8 rp = e.master ? load_raw(e.master, 1, 1, i, n) : load_raw(e.p, e.p_fp32, e.p_vec, i, n);
+    if (BITS == 32) {
+      const Raw8 rm = load_raw(e.avg, 1, 1, i, n), rv = load_raw(e.sq, 1, 1, i, n);
+      values(rm, 1, m);
+      values(rv, 1, v);
+    } else {
+      const uint2 cm = load_codes((const uint8_t*)e.avg, i, n), cv = load_codes((const uint8_t*)e.sq, i, n);
+      if (i < n) {
+        sm = e.savg[i >> 7];
+        sr = e.ssq[i >> 7];
+      }
+      code_values(cm, m);
+      code_values(cv, v);
     }
+    values(rg, e.g_fp32, g);
+    values(rp, e.master || e.p_fp32, p);
   }
-  const float keep = 1.0f - lr * e.wd;
   float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // Each product and sum rounded by itself: the moments' stored codes then depend on the formula alone.
-    const float gj = __fmul_rn(g[j], gs);
-    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.omb1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.omb2));
-    top = fmaxf(top, v[j]);
-  }
-  if (top < 1e37f) {
-    // sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2 (to the last place); zero for v = 0.
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float y;
-      asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v[j], 1e-37f)));
-      const float s = v[j] * y;
-      r[j] = fmaf(fmaf(-s, s, v[j]), 0.5f * y, s);
+  for (int j = 0; j < 4; ++j) {
+    if (BITS == 8) {
+      m[j] = mul2(m[j], both(sm));
+      v[j] = mul2(v[j], both(sr));
+      v[j] = mul2(v[j], v[j]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = sqrtf(v[j]);
+    // Each product and sum rounded by itself: the moments' stored codes then depend on the formula alone.
+    g[j] = mul2(g[j], both(c.gs));
+    m[j] = add2(mul2(m[j], both(a.b1)), mul2(g[j], both(a.omb1)));
+    v[j] = add2(mul2(v[j], both(a.b2)), mul2(mul2(g[j], g[j]), both(a.omb2)));
+    r[j] = root(v[j]);
+    if (BITS == 32) top = fmaxf(top, fmaxf(v[j].x, v[j].y));
   }
+  if (BITS == 8) {
+    sm = moment_scale(m);
+    sr = moment_scale(r);
+  }
+  // An infinite v (the square of a gradient above 1e19) has made its root NaN: the exact one instead.
+  if (BITS == 32 ? !(top < 3e38f) : __any_sync(0xffffffffu, !(sr < 3e38f))) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) p[j] = p[j] * keep - __fdividef(m[j] * lr1, fmaf(r[j], rbc2, a.eps));
+    for (int j = 0; j < 4; ++j) r[j] = make_float2(sqrtf(v[j].x), sqrtf(v[j].y));
+    if (BITS == 8) sr = moment_scale(r);
+  }
+  const float2 keep = both(1.0f - c.lr * e.wd);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 den = fma2(r[j], both(c.rbc2), both(a.eps));
+    p[j] = fma2(mul2(m[j], both(-c.lr1)), make_float2(reciprocal(den.x), reciprocal(den.y)), mul2(p[j], keep));
+  }
   if (e.master) store8(e.master, 1, 1, i, n, p);
   store8(e.p, e.p_fp32, e.p_vec, i, n, p);
   if (BITS == 32) {
@@ -385,27 +438,26 @@ __device__ __forceinline__ void update(const AdamTable& t, const AdamArgs& a, co
     store8(e.sq, 1, 1, i, n, v);
     return;
   }
-  const float sm = moment_scale(m), sr = moment_scale(r);
   uint2 cm = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), cr = cm;  // NaN codes
-  if (sm < 1e38f && sr < 1e38f) {
-    const float im = 1.0f / sm, ir = 1.0f / sr;
-    uint32_t wm[2] = {0, 0}, wr[2] = {0, 0};
+  if (sm < 1e37f && sr < 1e37f) {
+    const float im = inverse(sm), ir = inverse(sr);
+    uint32_t zm[8], zr[8];
     const uint32_t pair0 = e.index0 + (uint32_t)(i >> 1);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint32_t h = mix((pair0 + j / 2) ^ key);
-      const uint32_t u[2] = {h << 4 & 0xffff0u, h >> 12 & 0xffff0u};
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const float ym = quotient(m[j + d], sm, im), yr = quotient(r[j + d], sr, ir);
-        const uint32_t km = stochastic_code(ym, u[d]) | (__float_as_uint(ym) >> 24 & 0x80u);
-        const uint32_t kr = max(stochastic_code(yr, u[d]), r[j + d] > 0.f ? 1u : 0u);
-        wm[j / 4] |= km << (8 * (j % 4 + d));
-        wr[j / 4] |= kr << (8 * (j % 4 + d));
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t h = mix((pair0 + j) ^ c.key);
+      const uint32_t u0 = h << 4 & 0xffff0u, u1 = h >> 12 & 0xffff0u;
+      const float2 ym = quotient(m[j], sm, im), yr = quotient(r[j], sr, ir);
+      const float2 am = make_float2(fabsf(ym.x), fabsf(ym.y));
+      const float2 tm = add2(am, am), lm = add2(am, both(0.015625f)), tr = add2(yr, yr), lr = add2(yr, both(0.015625f));
+      zm[2 * j] = stochastic_code(tm.x, lm.x, u0, 0.f) | (__float_as_uint(ym.x) & 0x80000000u);
+      zm[2 * j + 1] = stochastic_code(tm.y, lm.y, u1, 0.f) | (__float_as_uint(ym.y) & 0x80000000u);
+      // sqrt(v) > 0 is held as code 1 at least
+      zr[2 * j] = stochastic_code(tr.x, lr.x, u0, r[j].x > 0.f ? 0.017578125f : 0.f);
+      zr[2 * j + 1] = stochastic_code(tr.y, lr.y, u1, r[j].y > 0.f ? 0.017578125f : 0.f);
     }
-    cm = make_uint2(wm[0], wm[1]);
-    cr = make_uint2(wr[0], wr[1]);
+    cm = make_uint2(top_bytes(zm[0], zm[1], zm[2], zm[3]), top_bytes(zm[4], zm[5], zm[6], zm[7]));
+    cr = make_uint2(top_bytes(zr[0], zr[1], zr[2], zr[3]), top_bytes(zr[4], zr[5], zr[6], zr[7]));
   }
   store_codes((uint8_t*)e.avg, i, n, cm);
   store_codes((uint8_t*)e.sq, i, n, cr);
@@ -416,28 +468,28 @@ __device__ __forceinline__ void update(const AdamTable& t, const AdamArgs& a, co
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamTable t, const AdamArgs a,
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamTable t, const AdamArgs a,
                                                             dora_adamw_control_t* __restrict__ control,
                                                             const float* __restrict__ grad_scale, int last) {
   pdl_trigger();
   pdl_wait();
   const int64_t step = control->step + 1;
-  const float lr = control->lr;
-  const float gs = grad_scale ? *grad_scale : 1.0f;
-  const bool run = isfinite(gs);
+  StepScalars sc;
+  sc.lr = control->lr;
+  sc.gs = grad_scale ? *grad_scale : 1.0f;
+  const bool run = isfinite(sc.gs);
   const Range range = cta_range(t.chunks);
   if (run && range.first < range.last) {
-    // The next chunk's loads are under way while this one is computed.
-    Elements<BITS> now, next;
-    fetch<BITS>(t, range.first, find_tensor(t, range.first), now);
     const float bc1 = -expm1f((float)step * a.ln_b1), bc2 = -expm1f((float)step * a.ln_b2);
-    const float lr1 = lr / bc1, rbc2 = 1.0f / sqrtf(bc2);
-    const uint32_t key = mix(a.seed + (uint32_t)step * 0x9E3779B9u);
+    sc.lr1 = sc.lr / bc1;
+    sc.rbc2 = 1.0f / sqrtf(bc2);
+    sc.key = mix(a.seed + (uint32_t)step * 0x9E3779B9u);
+    for (int c = range.first, k = find_tensor(t, range.first); c < range.last; ++k) {
+      const AdamEntry& e = t.e[k];
+      const int end = min(range.last, k + 1 < t.n ? t.first[k + 1] : t.chunks);
+      int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
 #pragma unroll 1
-    for (int c = range.first; c < range.last; ++c) {
-      if (c + 1 < range.last) fetch<BITS>(t, c + 1, now.k, next);
-      update<BITS>(t, a, now, gs, lr, lr1, rbc2, key);
-      now = next;
+      for (; c < end; ++c, i += kChunk) update<BITS>(e, a, sc, i);
     }
   }
   // The last CTA of the call's last launch counts the step: by then every CTA has read the count.
@@ -557,7 +609,7 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
   const AdamArgs a{(float)desc->beta1,          (float)(1.0 - desc->beta1),   (float)desc->beta2,
                    (float)(1.0 - desc->beta2),  (float)std::log(desc->beta1), (float)std::log(desc->beta2),
                    desc->eps,                   desc->seed};
-  const int most = device_sm_count() * 3;
+  const int most = device_sm_count() * 4;
   cudaError_t e = cudaSuccess;
   AdamTable t;
   int i = 0;
@@ -568,8 +620,8 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
       if (x.numel == 0) continue;
       t.first[t.n] = t.chunks;
       t.e[t.n++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.scale_avg, x.scale_sq, x.master, x.numel,
-                    (uint32_t)(x.index0 >> 1), x.weight_decay, x.param_dtype == DORA_FP32, x.grad_dtype == DORA_FP32,
-                    aligned16(x.param), aligned16(x.grad)};
+                    (uint32_t)(x.index0 >> 1), x.weight_decay, (uint8_t)(x.param_dtype == DORA_FP32),
+                    (uint8_t)(x.grad_dtype == DORA_FP32), (uint8_t)aligned16(x.param), (uint8_t)aligned16(x.grad)};
       t.chunks += (int)cdiv(x.numel, kChunk);
     }
     const int blocks = std::max(1, std::min(t.chunks, most));
