@@ -15,8 +15,8 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import _check, _ptr, _stream_ptr, _torch, load_library
-from .fp8 import _code, _current, _on
+from . import _check, _ptr, _torch, load_library
+from .fp8 import _WIDE, _code, _current, _empty, _stream
 
 
 class GradEntry(ctypes.Structure):
@@ -39,20 +39,13 @@ def _grad_table(grads, device):
     for i, g in enumerate(grads):
         if g.device != device:
             raise ValueError(f"gradient {i} is on {g.device}, expected {device}")
-    return (GradEntry * max(len(grads), 1))(*[GradEntry(_ptr(g), g.numel(), _code(g.dtype, f"gradient {i}", "w"))
+    return (GradEntry * max(len(grads), 1))(*[GradEntry(_ptr(g), g.numel(), _code(g.dtype, f"gradient {i}", _WIDE))
                                               for i, g in enumerate(grads)])
 
 
-def _grad_norm(table, n: int, max_norm: float, device, ws, stream):
-    torch = _torch()
-    lib = load_library()
-    with _on(stream):
-        out = torch.empty(2, dtype=torch.float32, device=device)
-        if ws is None:
-            ws = torch.empty(int(lib.dora_grad_norm_workspace_size(n)), dtype=torch.uint8, device=device)
-    _check(lib.dora_grad_norm(table, n, float(max_norm), out.data_ptr(), out.data_ptr() + 4, _ptr(ws),
-                              ws.numel() * ws.element_size(), _stream_ptr(stream)))
-    return out[0], out[1]
+def _grad_norm(table, n: int, max_norm: float, norm, scale, ws, device, stream) -> None:
+    _check(load_library().dora_grad_norm(table, n, max_norm, norm.data_ptr(), scale.data_ptr(), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream, device)))
 
 
 def dora_grad_norm(grads, max_norm: float = math.inf, *, ws=None, stream=None):
@@ -61,12 +54,18 @@ def dora_grad_norm(grads, max_norm: float = math.inf, *, ws=None, stream=None):
     norm = sqrt(sum of squares over all tensors); scale = min(1, max_norm /
     (norm + 1e-6)), NaN when the norm is not finite (DoraAdamW.step then skips).
     """
+    torch = _torch()
     grads = list(grads)
     if not grads:
         raise ValueError("grads is empty")
     device = grads[0].device
     _current(device)
-    return _grad_norm(_grad_table(grads, device), len(grads), max_norm, device, ws, stream)
+    table = _grad_table(grads, device)
+    norm, scale = (_empty((), torch.float32, device, stream) for _ in range(2))
+    if ws is None:
+        ws = _empty(int(load_library().dora_grad_norm_workspace_size(len(grads))), torch.uint8, device, stream)
+    _grad_norm(table, len(grads), float(max_norm), norm, scale, ws, device, stream)
+    return norm, scale
 
 
 class DoraAdamW:
@@ -101,7 +100,7 @@ class DoraAdamW:
                 raise ValueError(f"gradient {i} has shape {tuple(g.shape)}, expected {tuple(p.shape)}")
             if p.device != device:
                 raise ValueError(f"parameter {i} is on {p.device}, expected {device}")
-            _code(p.dtype, f"parameter {i}", "w")
+            _code(p.dtype, f"parameter {i}", _WIDE)
         self._grads = _grad_table(grads, device)
         spans = sorted((_ptr(p), p.numel() * p.element_size(), i) for i, p in enumerate(params) if p.numel())
         for (a, size, i), (b, _, j) in zip(spans, spans[1:]):
@@ -138,11 +137,15 @@ class DoraAdamW:
                 base["avg_scale"] + at // 32 if state_bits == 8 else None,
                 base["sq_scale"] + at // 32 if state_bits == 8 else None,
                 base["master"] + at_master * 4 if held else None, p.numel(), at, decay[i],
-                _code(p.dtype, f"parameter {i}", "w"), _code(g.dtype, f"gradient {i}", "w")))
+                _code(p.dtype, f"parameter {i}", _WIDE), _code(g.dtype, f"gradient {i}", _WIDE)))
             at += size
             at_master += size if held else 0
         self._tensors = (AdamwTensor * n)(*rows)
-        self._n, self._device, self._keep, self._ws = n, device, (params, grads), None
+        self._n, self._device, self._keep = n, device, (params, grads)
+        self._ref, self._control_ptr = ctypes.byref(self._desc), self._control.data_ptr()
+        # What a clipped step keeps between its kernels.
+        self._scale = torch.zeros((), **f32)
+        self._ws = torch.empty(int(load_library().dora_grad_norm_workspace_size(n)), dtype=torch.uint8, device=device)
 
     def set_lr(self, lr: float) -> None:
         """The learning rate of the steps queued from now on (written on the current stream)."""
@@ -154,10 +157,9 @@ class DoraAdamW:
         """dora_grad_norm of the bound gradients."""
         torch = _torch()
         _current(self._device)
-        if self._ws is None:
-            need = int(load_library().dora_grad_norm_workspace_size(self._n))
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self._device)
-        return _grad_norm(self._grads, self._n, max_norm, self._device, self._ws, stream)
+        norm, scale = (_empty((), torch.float32, self._device, stream) for _ in range(2))
+        _grad_norm(self._grads, self._n, float(max_norm), norm, scale, self._ws, self._device, stream)
+        return norm, scale
 
     def step(self, *, max_norm: float | None = None, grad_scale=None, stream=None):
         """One step from the bound gradients; returns their norm when max_norm is given.
@@ -167,17 +169,19 @@ class DoraAdamW:
         is not finite (a non-finite norm among them) skips the step.
         """
         torch = _torch()
-        _current(self._device)
+        device = self._device
+        _current(device)
         norm = None
         if max_norm is not None:
             if grad_scale is not None:
                 raise ValueError("give max_norm or grad_scale, not both")
-            norm, grad_scale = self.grad_norm(max_norm, stream=stream)
+            norm, grad_scale = _empty((), torch.float32, device, stream), self._scale
+            _grad_norm(self._grads, self._n, float(max_norm), norm, grad_scale, self._ws, device, stream)
         elif grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or
-                                         grad_scale.device != self._device):
-            raise ValueError(f"grad_scale must be one float32 value on {self._device}")
-        _check(load_library().dora_adamw(ctypes.byref(self._desc), self._tensors, self._n, _ptr(self._control),
-                                         _ptr(grad_scale), _stream_ptr(stream)))
+                                         grad_scale.device != device):
+            raise ValueError(f"grad_scale must be one float32 value on {device}")
+        _check(load_library().dora_adamw(self._ref, self._tensors, self._n, self._control_ptr, _ptr(grad_scale),
+                                         _stream(stream, device)))
         return norm
 
     def state_dict(self) -> dict:

@@ -55,8 +55,11 @@ struct GradEntry {
   int vec;
 };
 constexpr int kMaxGrads = 1100;
-using GradTable = Table<GradEntry, kMaxGrads>;
-static_assert(sizeof(GradTable) < 32000, "kernel parameters");
+template <int MAX>
+using GradTable = Table<GradEntry, MAX>;
+static_assert(sizeof(GradTable<kMaxGrads>) < 32000, "kernel parameters");
+// Calls of few tensors pass a short table: a full one costs the host 3 us more per launch.
+constexpr int kFew = 24;
 
 struct AdamEntry {
   void* p;
@@ -72,8 +75,9 @@ struct AdamEntry {
   uint8_t p_fp32, g_fp32, p_vec, g_vec;
 };
 constexpr int kMaxAdam = 385;
-using AdamTable = Table<AdamEntry, kMaxAdam>;
-static_assert(sizeof(AdamTable) < 32600, "kernel parameters");
+template <int MAX>
+using AdamTable = Table<AdamEntry, MAX>;
+static_assert(sizeof(AdamTable<kMaxAdam>) < 32600, "kernel parameters");
 
 // ------------------------------------------------------------------ two fp32 at a time
 
@@ -239,7 +243,8 @@ __device__ __forceinline__ double squares(const Raw8& raw, int fp32) {
 }
 
 // Sum of squares of this CTA's chunks: 8 values in fp32, everything above in double.
-__global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __grid_constant__ GradTable t,
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __grid_constant__ GradTable<MAX> t,
                                                                      double* __restrict__ part) {
   __shared__ double red[kThreads / 32];
   pdl_trigger();
@@ -467,8 +472,8 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamTable t, const AdamArgs a,
+template <int BITS, int MAX>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamTable<MAX> t, const AdamArgs a,
                                                             dora_adamw_control_t* __restrict__ control,
                                                             const float* __restrict__ grad_scale, int last) {
   pdl_trigger();
@@ -511,7 +516,53 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 std::string nth(const char* what, int i) { return std::string("tensor ") + std::to_string(i) + ": " + what; }
 
+// check_ptr of tensor i; the message is made only for a pointer that is refused.
+bool check_nth(const void* p, const char* name, int i, size_t align) {
+  return (p && reinterpret_cast<uintptr_t>(p) % align == 0) || check_ptr(p, nth(name, i).c_str(), align);
+}
+
 constexpr int64_t kMaxNumel = int64_t(1) << 40;
+
+// One launch over the tensors from i on, as many as the table holds.
+template <int MAX>
+cudaError_t launch_norm(const dora_grad_t* grads, int n_tensors, int most, double* part, int& parts, int& i,
+                        cudaStream_t st) {
+  GradTable<MAX> t;
+  t.n = t.chunks = 0;
+  for (; i < n_tensors && t.n < MAX; ++i) {
+    const dora_grad_t& g = grads[i];
+    if (g.numel == 0) continue;
+    t.first[t.n] = t.chunks;
+    t.e[t.n++] = {g.grad, g.numel, g.dtype == DORA_FP32, aligned16(g.grad)};
+    t.chunks += (int)cdiv(g.numel, kChunk);
+  }
+  if (t.n == 0) return cudaSuccess;
+  const int blocks = std::min(t.chunks, most);
+  double* to = part + parts;
+  parts += blocks;
+  ProfRange pr("grad_norm_partial", st);
+  return launch_pdl(grad_norm_partial_kernel<MAX>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, to);
+}
+
+template <int BITS, int MAX>
+cudaError_t launch_adamw(const AdamArgs& a, const dora_adamw_tensor_t* tensors, int n_tensors, int& i,
+                         dora_adamw_control_t* control, const float* grad_scale, cudaStream_t st) {
+  AdamTable<MAX> t;
+  t.n = t.chunks = 0;
+  for (; i < n_tensors && t.n < MAX; ++i) {
+    const dora_adamw_tensor_t& x = tensors[i];
+    if (x.numel == 0) continue;
+    t.first[t.n] = t.chunks;
+    t.e[t.n++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.scale_avg, x.scale_sq, x.master, x.numel,
+                  (uint32_t)(x.index0 >> 1), x.weight_decay, (uint8_t)(x.param_dtype == DORA_FP32),
+                  (uint8_t)(x.grad_dtype == DORA_FP32), (uint8_t)aligned16(x.param), (uint8_t)aligned16(x.grad)};
+    t.chunks += (int)cdiv(x.numel, kChunk);
+  }
+  const int blocks = std::max(1, std::min(t.chunks, device_sm_count() * 4));
+  ProfRange pr(BITS == 8 ? "adamw8" : "adamw32", st);
+  return launch_pdl(adamw_kernel<BITS, MAX>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, a, control, grad_scale,
+                    i == n_tensors ? 1 : 0);
+}
 
 }  // namespace
 }  // namespace dora
@@ -535,7 +586,7 @@ dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, float max_
     const dora_grad_t& g = grads[i];
     if (g.numel < 0 || g.numel > kMaxNumel) return set_error(nth("numel out of range", i)), DORA_EINVAL;
     if (!is_wide(g.dtype)) return set_error(nth("dtype is not DORA_BF16 or DORA_FP32", i)), DORA_EINVAL;
-    if (g.numel > 0 && !check_ptr(g.grad, nth("grad", i).c_str(), width(g.dtype))) return DORA_EINVAL;
+    if (g.numel > 0 && !check_nth(g.grad, "grad", i, width(g.dtype))) return DORA_EINVAL;
     total += cdiv(g.numel, kChunk);
   }
   if (total > INT32_MAX) return set_error("too many elements for one call"), DORA_EINVAL;
@@ -547,24 +598,9 @@ dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, float max_
   const int most = std::min(kNormBlocksMax, device_sm_count() * kNormBlocksPerSM);
   int parts = 0;
   cudaError_t e = cudaSuccess;
-  GradTable t;
-  for (int i = 0; i < n_tensors && e == cudaSuccess;) {
-    t.n = t.chunks = 0;
-    for (; i < n_tensors && t.n < kMaxGrads; ++i) {
-      const dora_grad_t& g = grads[i];
-      if (g.numel == 0) continue;
-      t.first[t.n] = t.chunks;
-      t.e[t.n++] = {g.grad, g.numel, g.dtype == DORA_FP32, aligned16(g.grad)};
-      t.chunks += (int)cdiv(g.numel, kChunk);
-    }
-    if (t.n == 0) break;
-    const int blocks = std::min(t.chunks, most);
-    {
-      ProfRange pr("grad_norm_partial", st);
-      e = launch_pdl(grad_norm_partial_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, part + parts);
-    }
-    parts += blocks;
-  }
+  for (int i = 0; i < n_tensors && e == cudaSuccess;)
+    e = n_tensors <= kFew ? launch_norm<kFew>(grads, n_tensors, most, part, parts, i, st)
+                          : launch_norm<kMaxGrads>(grads, n_tensors, most, part, parts, i, st);
   if (e == cudaSuccess) {
     ProfRange pr("grad_norm_final", st);
     e = launch_pdl(grad_norm_final_kernel, dim3(1), dim3(kThreads), 0, st, (const double*)part, parts, max_norm, norm,
@@ -593,13 +629,10 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
     if (x.index0 < 0 || x.index0 % 8) return set_error(nth("index0 is not a multiple of 8", i)), DORA_EINVAL;
     total += cdiv(x.numel, kChunk);
     if (x.numel == 0) continue;
-    if (!check_ptr(x.param, nth("param", i).c_str(), width(x.param_dtype)) ||
-        !check_ptr(x.grad, nth("grad", i).c_str(), width(x.grad_dtype)) ||
-        !check_ptr(x.exp_avg, nth("exp_avg", i).c_str(), 16) ||
-        !check_ptr(x.exp_avg_sq, nth("exp_avg_sq", i).c_str(), 16) ||
-        !check_opt_ptr(x.master, nth("master", i).c_str(), 16) ||
-        (eight && (!check_ptr(x.scale_avg, nth("scale_avg", i).c_str(), 4) ||
-                   !check_ptr(x.scale_sq, nth("scale_sq", i).c_str(), 4))))
+    if (!check_nth(x.param, "param", i, width(x.param_dtype)) || !check_nth(x.grad, "grad", i, width(x.grad_dtype)) ||
+        !check_nth(x.exp_avg, "exp_avg", i, 16) || !check_nth(x.exp_avg_sq, "exp_avg_sq", i, 16) ||
+        (x.master && !check_nth(x.master, "master", i, 16)) ||
+        (eight && (!check_nth(x.scale_avg, "scale_avg", i, 4) || !check_nth(x.scale_sq, "scale_sq", i, 4))))
       return DORA_EINVAL;
   }
   if (total > INT32_MAX) return set_error("too many elements for one call"), DORA_EINVAL;
@@ -609,26 +642,14 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
   const AdamArgs a{(float)desc->beta1,          (float)(1.0 - desc->beta1),   (float)desc->beta2,
                    (float)(1.0 - desc->beta2),  (float)std::log(desc->beta1), (float)std::log(desc->beta2),
                    desc->eps,                   desc->seed};
-  const int most = device_sm_count() * 4;
-  cudaError_t e = cudaSuccess;
-  AdamTable t;
+  const bool few = n_tensors <= kFew;
+  cudaError_t e;
   int i = 0;
   do {
-    t.n = t.chunks = 0;
-    for (; i < n_tensors && t.n < kMaxAdam; ++i) {
-      const dora_adamw_tensor_t& x = tensors[i];
-      if (x.numel == 0) continue;
-      t.first[t.n] = t.chunks;
-      t.e[t.n++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.scale_avg, x.scale_sq, x.master, x.numel,
-                    (uint32_t)(x.index0 >> 1), x.weight_decay, (uint8_t)(x.param_dtype == DORA_FP32),
-                    (uint8_t)(x.grad_dtype == DORA_FP32), (uint8_t)aligned16(x.param), (uint8_t)aligned16(x.grad)};
-      t.chunks += (int)cdiv(x.numel, kChunk);
-    }
-    const int blocks = std::max(1, std::min(t.chunks, most));
-    const int last = i == n_tensors;
-    ProfRange pr(eight ? "adamw8" : "adamw32", st);
-    e = launch_pdl(eight ? adamw_kernel<8> : adamw_kernel<32>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, a,
-                   control, grad_scale, last);
+    e = eight ? (few ? launch_adamw<8, kFew>(a, tensors, n_tensors, i, control, grad_scale, st)
+                     : launch_adamw<8, kMaxAdam>(a, tensors, n_tensors, i, control, grad_scale, st))
+              : (few ? launch_adamw<32, kFew>(a, tensors, n_tensors, i, control, grad_scale, st)
+                     : launch_adamw<32, kMaxAdam>(a, tensors, n_tensors, i, control, grad_scale, st));
   } while (i < n_tensors && e == cudaSuccess);
   return cuda_status(e, "dora_adamw");
 }

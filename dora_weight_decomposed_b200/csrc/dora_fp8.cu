@@ -16,91 +16,6 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // ------------------------------------------------------------------ quantisation
 
-// max(a, |b|) that keeps a NaN.
-__device__ __forceinline__ float absmax_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-  return r;
-}
-
-// The scale of a block and its inverse. Both are powers of two, read off the
-// exponent of amax: amax = 1.f 2^x fits top = 1.75 2^k at e = x - k when
-// 1.f <= 1.75, else at x - k + 1. Non-finite: scale = amax, inverse 0 (inf) or NaN.
-struct BlockScale {
-  float scale, inv;
-};
-template <bool E5M2>
-__device__ __forceinline__ BlockScale block_scale(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  if (u >= 0x7f800000u) return {amax, 1.0f / amax};
-  int e = (int)(u >> 23) - 127 - (E5M2 ? 15 : 8) + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = max(e, -126);
-  return {__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23)};
-}
-
-// Two values to 8-bit codes, rounded to nearest even (the scale keeps them in range; NaN stays NaN).
-template <bool E5M2>
-__device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi) {
-  uint16_t r;
-  if (E5M2)
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <bool E5M2>
-__device__ __forceinline__ uint2 to_fp8x8(const float* v, float inv) {
-  uint2 r;
-  r.x = to_fp8x2<E5M2>(v[0] * inv, v[1] * inv) | to_fp8x2<E5M2>(v[2] * inv, v[3] * inv) << 16;
-  r.y = to_fp8x2<E5M2>(v[4] * inv, v[5] * inv) | to_fp8x2<E5M2>(v[6] * inv, v[7] * inv) << 16;
-  return r;
-}
-
-// Eight consecutive values as they lie in memory (a bf16 thread holds half the registers that fp32 would take).
-struct Raw8Bf16 {
-  uint4 u;
-  __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ void clear() { u = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ float absmax() const {  // NaN if one is
-    uint32_t m;
-    asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"
-        : "=r"(m)
-        : "r"(u.x & 0x7fff7fffu), "r"(u.y & 0x7fff7fffu), "r"(u.z & 0x7fff7fffu), "r"(u.w & 0x7fff7fffu));
-    return absmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-  }
-  __device__ void values(float* v) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
-struct Raw8Float {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ float absmax() const {
-    float v[8], m = 0.f;
-    values(v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = absmax_nan(m, v[i]);
-    return m;
-  }
-  __device__ void values(float* v) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-};
-template <class T>
-struct Raw8 : Raw8Float {};
-template <>
-struct Raw8<__nv_bfloat16> : Raw8Bf16 {};
-
 // 1 x 128 blocks. It lets the next grid start only once all work before it is done, so that a product which
 // follows it may read the weight at once. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
 // in flight; the CTA's eight warps take neighbouring column blocks. Bound by HBM.
@@ -219,7 +134,7 @@ cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t
 
 // Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
 // answer of the occupancy query, which counts one CTA per SM for the narrow kernels; asked once per device.
-template <int NT, bool W_MN>
+template <int NT, bool W_MN, class XT>
 int clusters_alone(int cs) {
   static std::atomic<int> known[64][9];
   int dev = 0;
@@ -236,7 +151,7 @@ int clusters_alone(int cs) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, XT>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = std::max(1, device_sm_count() / cs * 7 / 8);
     }
@@ -248,21 +163,21 @@ int clusters_alone(int cs) {
 
 // The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two, and 256
 // CTAs of one launch were seen to start together): twice as many, or one on every (cs + 1) / 2 SMs.
-template <int NT, bool W_MN>
+template <int NT, bool W_MN, class XT>
 int narrow_slots(int cs) {
-  return std::max(2 * clusters_alone<NT, W_MN>(cs), clusters_alone<NT, W_MN>((cs + 1) / 2));
+  return std::max(2 * clusters_alone<NT, W_MN, XT>(cs), clusters_alone<NT, W_MN, XT>((cs + 1) / 2));
 }
 
 // CTAs per tile of the narrow kernel (K splits, one cluster): the count with the least estimated time, in k-blocks:
 // waves of clusters times the k-blocks of a split plus what a CTA costs beside them, 2 to start and fill and 2 more
 // to add the splits. T = 37 of 27648 x 5120 takes 31.3 us with its 216 tiles in one wave, 36.5 us with two splits
 // and 432 CTAs in two waves; T = 16 of 8192 x 8192 17.7 us with 4 splits (256 CTAs), 22.3 us with 8 (two waves).
-template <int NT, bool W_MN>
+template <int NT, bool W_MN, class XT>
 int narrow_splits(int64_t tiles, int64_t nkb) {
   int best = 1;
   double best_t = 1e300;
   for (int cs = 1; cs <= 8 && cs <= nkb; ++cs) {
-    const double t = (double)cdiv(tiles, narrow_slots<NT, W_MN>(cs)) * ((double)cdiv(nkb, cs) + (cs > 1 ? 4.0 : 2.0));
+    const double t = (double)cdiv(tiles, narrow_slots<NT, W_MN, XT>(cs)) * ((double)cdiv(nkb, cs) + (cs > 1 ? 4.0 : 2.0));
     if (t < best_t - 1e-9) {
       best_t = t;
       best = cs;
@@ -271,14 +186,14 @@ int narrow_splits(int64_t tiles, int64_t nkb) {
   return best;
 }
 
-template <int NT, bool W_MN>
+template <int NT, bool W_MN, class XT>
 cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp8Geom& g, bool early_w, cudaStream_t st) {
-  auto kern = fp8_narrow_kernel<NT, W_MN>;
+  auto kern = fp8_narrow_kernel<NT, W_MN, XT>;
   static std::atomic<unsigned long long> smem_set{0};
   cudaError_t e = set_smem_once(smem_set, kern, Fp8Narrow<NT>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
-  const int cs = narrow_splits<NT, W_MN>(tiles * t_tiles, g.nkb);
+  const int cs = narrow_splits<NT, W_MN, XT>(tiles * t_tiles, g.nkb);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * t_tiles * cs));
   cfg.blockDim = dim3(kF8Threads);
@@ -300,9 +215,9 @@ template <bool W_MN>
 cudaError_t launch_narrow_nt(int nt, const CUtensorMap& tw, const CUtensorMap& tx, const Fp8Geom& g, bool early_w,
                              cudaStream_t st) {
   switch (nt) {
-    case 16: return launch_narrow<16, W_MN>(tw, tx, g, early_w, st);
-    case 32: return launch_narrow<32, W_MN>(tw, tx, g, early_w, st);
-    default: return launch_narrow<64, W_MN>(tw, tx, g, early_w, st);
+    case 16: return launch_narrow<16, W_MN, void>(tw, tx, g, early_w, st);
+    case 32: return launch_narrow<32, W_MN, void>(tw, tx, g, early_w, st);
+    default: return launch_narrow<64, W_MN, void>(tw, tx, g, early_w, st);
   }
 }
 
@@ -326,8 +241,9 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
   return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, tout, g);
 }
 
-// What a call keeps in its workspace: the quantised operand and its scales.
+// What a call keeps in its workspace (the quantised operand and its scales), unless the kernel quantises it itself.
 struct Fp8Plan {
+  bool own_x = false;
   size_t off_q = 0, off_s = 0, total = 0;
 };
 
@@ -336,15 +252,18 @@ bool is_wide(dora_dtype_t t) { return t == DORA_BF16 || t == DORA_FP32; }
 
 Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
   Fp8Plan p;
-  const int64_t K = op == DORA_FP8_OP_FORWARD ? d.d_in : d.d_out;
-  size_t off = 0;
-  if (!is_fp8(d.in_dtype) && T > 0) {
-    p.off_q = off;
-    off += align256((size_t)T * K);
-    p.off_s = off;
-    off += align256((size_t)T * cdiv(K, 128) * 4);
+  const bool back = op == DORA_FP8_OP_BACKWARD, bf16 = d.in_dtype == DORA_BF16;
+  const int64_t K = back ? d.d_out : d.d_in, N = back ? d.d_in : d.d_out, nkb = cdiv(K, 128);
+  if (is_fp8(d.in_dtype) || T == 0) return p;
+  if (T <= 16 && nkb <= 8 * Fp8Narrow<16>::STAGES) {
+    const int64_t tiles = cdiv(N, 128);
+    const int cs = back ? (bf16 ? narrow_splits<16, true, __nv_bfloat16>(tiles, nkb) : narrow_splits<16, true, float>(tiles, nkb))
+                        : (bf16 ? narrow_splits<16, false, __nv_bfloat16>(tiles, nkb) : narrow_splits<16, false, float>(tiles, nkb));
+    p.own_x = cdiv(nkb, cs) <= Fp8Narrow<16>::STAGES;
   }
-  p.total = off;
+  if (p.own_x) return p;
+  p.off_s = align256((size_t)T * K);
+  p.total = p.off_s + align256((size_t)T * nkb * 4);
   return p;
 }
 
@@ -379,23 +298,33 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   if (T == 0) return DORA_OK;
   const char* where = backward ? "dora_fp8_backward" : "dora_fp8_forward";
   const int64_t K = backward ? desc->d_out : desc->d_in, N = backward ? desc->d_in : desc->d_out;
-  dora_dtype_t type = desc->in_dtype;
-  if (!given) {
+  const dora_dtype_t type = given ? desc->in_dtype : desc->fp8_dtype;
+  const void* xq = x;
+  if (!given && !p.own_x) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-    type = desc->fp8_dtype;
     const cudaError_t e = quantize(T, K, desc->in_dtype, type, false, x, w + p.off_q, reinterpret_cast<float*>(w + p.off_s), st);
     if (e != cudaSuccess) return cuda_status(e, where);
-    x = w + p.off_q;
+    xq = w + p.off_q;
     x_scale = reinterpret_cast<const float*>(w + p.off_s);
   }
   const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
-  Fp8Geom g{x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
+  Fp8Geom g{x, (int)K, x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
             desc->out_dtype == DORA_FP32, type == DORA_E5M2};
+  CUtensorMap tx, tw;
+  cudaError_t e = make_map_2d(&tw, W, desc->d_out, desc->d_in, 1, 128);
+  if (e != cudaSuccess) return cuda_status(e, where);
+  if (p.own_x) {
+    if (desc->in_dtype == DORA_BF16)
+      e = backward ? launch_narrow<16, true, __nv_bfloat16>(tw, tw, g, false, st)
+                   : launch_narrow<16, false, __nv_bfloat16>(tw, tw, g, false, st);
+    else
+      e = backward ? launch_narrow<16, true, float>(tw, tw, g, false, st)
+                   : launch_narrow<16, false, float>(tw, tw, g, false, st);
+    return cuda_status(e, where);
+  }
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
   const bool narrow = T <= 128;
-  CUtensorMap tx, tw;
-  cudaError_t e = make_map_2d(&tx, x, T, K, 1, narrow ? nt : 128);
-  if (e == cudaSuccess) e = make_map_2d(&tw, W, desc->d_out, desc->d_in, 1, 128);
+  e = make_map_2d(&tx, xq, T, K, 1, narrow ? nt : 128);
   if (e == cudaSuccess) {
     if (narrow)
       e = backward ? launch_narrow_nt<true>(nt, tw, tx, g, !given, st) : launch_narrow_nt<false>(nt, tw, tx, g, !given, st);

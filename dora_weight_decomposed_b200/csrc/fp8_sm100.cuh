@@ -9,14 +9,107 @@
 // tile's. Two accumulators let the MMAs of the next k-block run meanwhile.
 #pragma once
 
+#include <type_traits>
+
 #include "sm100_ptx.cuh"
 
 namespace dora {
+
+// ------------------------------------------------------------------ block scales and codes
+
+// max(a, |b|) that keeps a NaN.
+__device__ __forceinline__ float absmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The scale of a block and its inverse. Both are powers of two, read off the
+// exponent of amax: amax = 1.f 2^x fits top = 1.75 2^k at e = x - k when
+// 1.f <= 1.75, else at x - k + 1. Non-finite: scale = amax, inverse 0 (inf) or NaN.
+struct BlockScale {
+  float scale, inv;
+};
+template <bool E5M2>
+__device__ __forceinline__ BlockScale block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u >= 0x7f800000u) return {amax, 1.0f / amax};
+  int e = (int)(u >> 23) - 127 - (E5M2 ? 15 : 8) + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, -126);
+  return {__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23)};
+}
+
+// Two values to 8-bit codes, rounded to nearest even (the scale keeps them in range; NaN stays NaN).
+template <bool E5M2>
+__device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi) {
+  uint16_t r;
+  if (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint2 to_fp8x8(const float* v, float inv) {
+  uint2 r;
+  r.x = to_fp8x2<E5M2>(v[0] * inv, v[1] * inv) | to_fp8x2<E5M2>(v[2] * inv, v[3] * inv) << 16;
+  r.y = to_fp8x2<E5M2>(v[4] * inv, v[5] * inv) | to_fp8x2<E5M2>(v[6] * inv, v[7] * inv) << 16;
+  return r;
+}
+
+// Eight consecutive values as they lie in memory (a bf16 thread holds half the registers that fp32 would take).
+struct Raw8Bf16 {
+  uint4 u;
+  __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ void clear() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ float absmax() const {  // NaN if one is
+    uint32_t m;
+    asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"
+        : "=r"(m)
+        : "r"(u.x & 0x7fff7fffu), "r"(u.y & 0x7fff7fffu), "r"(u.z & 0x7fff7fffu), "r"(u.w & 0x7fff7fffu));
+    return absmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ void values(float* v) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+struct Raw8Float {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ float absmax() const {
+    float v[8], m = 0.f;
+    values(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = absmax_nan(m, v[i]);
+    return m;
+  }
+  __device__ void values(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <class T>
+struct Raw8 : Raw8Float {};
+template <>
+struct Raw8<__nv_bfloat16> : Raw8Bf16 {};
+
+// ------------------------------------------------------------------ products
 
 constexpr int kF8BK = 128;  // K per block: one 128-byte swizzle row, one scale
 constexpr int kF8Threads = 192;
 
 struct Fp8Geom {
+  const void* x;     // bf16 or fp32 [T x K] where a kernel quantises it itself
+  int K;
   const float* xs;   // [kb][T]
   const float* ws;   // the weight's scales: n block * ws_n + k block * ws_k
   void* out;         // [T x N]
@@ -56,7 +149,8 @@ struct Fp8Narrow {
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = 16384 + X_BYTES;
   static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4;
-  static constexpr int SCALE_BYTES = 4 * 2 * NT * 4;  // per folding warp: two k-blocks' token scales
+  static constexpr int SCALE_BYTES = 8 * NT * 4;  // token scales: two k-blocks per folding warp, or one per stage
+  static_assert(STAGES <= 8, "scales");
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES + 256 + 1024;
   static constexpr uint32_t ACC_COLS = NT < 32 ? 16 : NT;  // two accumulators; TMEM comes in 32 columns at least
   static_assert(NT * 128 * 4 <= STAGES * STAGE_BYTES, "the splits' sums fit the ring");
@@ -89,7 +183,11 @@ __device__ __forceinline__ void fp8_reduce_splits(const Fp8Geom& g, const float*
   }
 }
 
-template <int NT, bool W_MN>
+// XT: the type of x that the kernel quantises itself, or void where x comes in codes through tX. For up to 16 tokens
+// and no more k-blocks per CTA than the ring has stages, the folding warps turn the CTA's blocks of x into codes while
+// the weight is on its way, which saves a launch, its latency and the workspace. (Doing so inside a longer loop costs
+// more than the launch: T = 1 of 27648 x 5120, 40 blocks per CTA, took 40 us so and 27 us with the launch.)
+template <int NT, bool W_MN, class XT>
 __global__ void __launch_bounds__(kF8Threads, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX, const Fp8Geom g,
                       int cs, int early_w) {
@@ -104,6 +202,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   uint64_t* acce = accf + 2;        // [2] accumulator folded
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
 
+  constexpr bool OWN_X = !std::is_same<XT, void>::value;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = blockIdx.x % cs;  // the cluster's CTAs are neighbours in x
@@ -114,7 +213,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], OWN_X ? 5 : 1);  // the loads, and the four warps that write x
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -123,7 +222,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     }
     fence_mbar_init();
     prefetch_tmap(&tW);
-    prefetch_tmap(&tX);
+    if (!OWN_X) prefetch_tmap(&tX);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 2 * Cfg::ACC_COLS);
@@ -145,7 +244,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       // before that grid is done.
       auto load_w = [&](int i) {
         uint8_t* sw = smem + i % STAGES * Cfg::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[i % STAGES], Cfg::STAGE_BYTES);
+        mbar_arrive_expect_tx(&full[i % STAGES], OWN_X ? 16384 : Cfg::STAGE_BYTES);
         if (!W_MN)
           tma_load_2d(sw, &tW, &full[i % STAGES], (kb0 + i) * kF8BK, n0);
         else
@@ -162,7 +261,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
           if (!mbar_wait(&empty[s], ((uint32_t)(i / STAGES) & 1u) ^ 1u)) break;
           load_w(i);
         }
-        tma_load_2d(smem + s * Cfg::STAGE_BYTES + 16384, &tX, &full[s], (kb0 + i) * kF8BK, t0);
+        if (!OWN_X) tma_load_2d(smem + s * Cfg::STAGE_BYTES + 16384, &tX, &full[s], (kb0 + i) * kF8BK, t0);
       }
       if (i < nkb)  // a wait ran out: let the copies in flight land before the shared memory goes
         for (int j = max(0, i - STAGES); j < i; ++j) mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, kWaitLimitNs / 16);
@@ -189,32 +288,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   } else {
     if (early_w) pdl_wait();
     const int q = warp & 3;
-    constexpr int NS = (NT + 31) / 32;
     const float* ws = g.ws + (size_t)(n0 >> 7) * g.ws_n + (size_t)kb0 * g.ws_k;
-    // Lane l fetches the scales of tokens l, l + 32, ... one k-block ahead; every lane reads them back from the warp's
-    // own piece of shared memory, four at a time.
-    float* mine = scales + q * 2 * NT;
-    float xn[NS], wn = 0.f;
-    auto fetch = [&](int i) {
-      wn = ws[(size_t)i * g.ws_k];
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        const int t = t0 + 32 * j + lane;
-        xn[j] = t < g.T ? g.xs[(size_t)(kb0 + i) * g.T + t] : 0.f;
-      }
-    };
-    if (nkb > 0) fetch(0);
-#pragma unroll 1
-    for (int i = 0; i < nkb; ++i) {
-      const int b = i & 1;
-      const float* sc = mine + b * NT;
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (NT >= 32 || lane < NT) mine[b * NT + 32 * j + lane] = xn[j] * wn;
-      __syncwarp();
-      if (i + 1 < nkb) fetch(i + 1);
-      if (!mbar_wait(&accf[b], (uint32_t)(i >> 1) & 1u)) break;
-      tc_fence_after();
+    auto fold = [&](int b, const float* sc) {
       const uint32_t ta = tmem + b * Cfg::ACC_COLS + ((uint32_t)(q * 32) << 16);
 #pragma unroll
       for (int c = 0; c < NT / 16; ++c) {
@@ -232,6 +307,83 @@ __global__ void __launch_bounds__(kF8Threads, 2)
           fma2(acc[8 * c + 2 * j], v[4 * j], v[4 * j + 1], s4.x, s4.y);
           fma2(acc[8 * c + 2 * j + 1], v[4 * j + 2], v[4 * j + 3], s4.z, s4.w);
         }
+      }
+    };
+    if constexpr (OWN_X) {
+      // Eight threads of 16 values make one token's block. Rows behind the last token stay as they are: they only
+      // reach columns of D that nobody reads.
+      const int tid = threadIdx.x - 64, t = tid >> 3, c = (tid & 7) * 16;
+      const XT* x = reinterpret_cast<const XT*>(g.x) + (size_t)min(t0 + t, g.T - 1) * g.K;
+      Raw8<XT> raw[STAGES][2];
+      float w[STAGES];
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) {
+        const int k = (kb0 + i) * kF8BK + c;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (i < nkb && k < g.K)  // K is a multiple of 16
+            raw[i][j].load(x + k + 8 * j);
+          else
+            raw[i][j].clear();
+        }
+        w[i] = i < nkb ? ws[(size_t)i * g.ws_k] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) {
+        if (i >= nkb) break;
+        float amax = absmax_nan(raw[i][0].absmax(), raw[i][1].absmax());
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const BlockScale bs = g.a_e5m2 ? block_scale<true>(amax) : block_scale<false>(amax);
+        if (t0 + t < g.T) {
+          uint2 code[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float v[8];
+            raw[i][j].values(v);
+            code[j] = g.a_e5m2 ? to_fp8x8<true>(v, bs.inv) : to_fp8x8<false>(v, bs.inv);
+          }
+          uint8_t* row = smem + i * Cfg::STAGE_BYTES + 16384 + t * 128;
+          *reinterpret_cast<uint4*>(row + (((tid & 7) ^ (t & 7)) << 4)) = make_uint4(code[0].x, code[0].y, code[1].x, code[1].y);
+          if ((tid & 7) == 0) scales[i * NT + t] = bs.scale * w[i];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[i]);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps' scales
+#pragma unroll 1
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait(&accf[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+        tc_fence_after();
+        fold(i & 1, scales + i * NT);
+      }
+    } else {
+      constexpr int NS = (NT + 31) / 32;
+      // Lane l fetches the scales of tokens l, l + 32, ... one k-block ahead; every lane reads them back from the warp's
+      // own piece of shared memory, four at a time.
+      float* mine = scales + q * 2 * NT;
+      float xn[NS], wn = 0.f;
+      auto fetch = [&](int i) {
+        wn = ws[(size_t)i * g.ws_k];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int t = t0 + 32 * j + lane;
+          xn[j] = t < g.T ? g.xs[(size_t)(kb0 + i) * g.T + t] : 0.f;
+        }
+      };
+      if (nkb > 0) fetch(0);
+#pragma unroll 1
+      for (int i = 0; i < nkb; ++i) {
+        const int b = i & 1;
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          if (NT >= 32 || lane < NT) mine[b * NT + 32 * j + lane] = xn[j] * wn;
+        __syncwarp();
+        if (i + 1 < nkb) fetch(i + 1);
+        if (!mbar_wait(&accf[b], (uint32_t)(i >> 1) & 1u)) break;
+        tc_fence_after();
+        fold(b, mine + b * NT);
       }
     }
   }

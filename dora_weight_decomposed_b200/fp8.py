@@ -12,8 +12,8 @@ include/dora.h for the formulas.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 from . import _check, _ptr, _shape, _stream_ptr, _torch, load_library
 
@@ -27,24 +27,32 @@ class Fp8Desc(ctypes.Structure):
                 ("fp8_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
-def _code(dtype, name: str, kinds: str) -> int:
-    """The C dtype code; kinds: "w" bf16 and fp32, "8" the 8-bit floats, or both."""
+_WIDE: dict = {}   # dtype -> C code, filled on first use (torch is imported late)
+_EIGHT: dict = {}
+_BOTH: dict = {}
+
+
+def _codes() -> None:
     torch = _torch()
-    codes = {}
-    if "w" in kinds:
-        codes.update({torch.bfloat16: 0, torch.float32: 1})
-    if "8" in kinds:
-        codes.update({torch.float8_e4m3fn: DORA_E4M3, torch.float8_e5m2: DORA_E5M2})
-    if dtype not in codes:
-        raise TypeError(f"{name} is {dtype}, expected one of {', '.join(str(d) for d in codes)}")
-    return codes[dtype]
+    _WIDE.update({torch.bfloat16: 0, torch.float32: 1})
+    _EIGHT.update({torch.float8_e4m3fn: DORA_E4M3, torch.float8_e5m2: DORA_E5M2})
+    _BOTH.update({**_WIDE, **_EIGHT})
+
+
+def _code(dtype, name: str, among: dict) -> int:
+    """The C dtype code, of the types in `among`."""
+    if not _BOTH:
+        _codes()
+    code = among.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} is {dtype}, expected one of {', '.join(str(d) for d in among)}")
+    return code
 
 
 def _tensor(t, shape, dtype, device, name: str) -> None:
-    """Shape, dtype and device of one tensor (None is skipped): the C ABI cannot see them."""
-    if t is None:
-        return
-    _shape(t, shape, name)
+    """Shape, dtype and device of one tensor: the C ABI cannot see them."""
+    if t.shape != shape:
+        _shape(t, shape, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
@@ -52,15 +60,29 @@ def _tensor(t, shape, dtype, device, name: str) -> None:
 
 
 def _current(device) -> None:
+    if device.type == "cuda":
+        torch = _torch()
+        if device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}; "
+                             f"call under torch.cuda.device({device.index})")
+
+
+def _stream(stream, device):
+    """_stream_ptr, without building a stream object for the current stream (a third of a small call's host time)."""
+    if stream is None and device.type == "cuda":
+        raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(device.index) or None
+    return _stream_ptr(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream that uses it."""
     torch = _torch()
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}; "
-                         f"call under torch.cuda.device({device.index})")
-
-
-def _on(stream):
-    """What is allocated for a call belongs to the stream that uses it."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def dora_fp8_quantize(x, *, block: str = "row", dtype=None, q=None, scale=None, stream=None):
@@ -77,59 +99,85 @@ def dora_fp8_quantize(x, *, block: str = "row", dtype=None, q=None, scale=None, 
     if x.dim() != 2:
         raise ValueError(f"x has {x.dim()} dimensions, expected 2")
     dtype = torch.float8_e4m3fn if dtype is None else dtype
-    code, out = _code(x.dtype, "x", "w"), _code(dtype, "dtype", "8")
+    code, out = _code(x.dtype, "x", _WIDE), _code(dtype, "dtype", _EIGHT)
     rows, cols = x.shape
-    up = lambda n: -(-n // 128)
-    shape = (up(cols), rows) if block == "row" else (up(rows), up(cols))
-    _current(x.device)
-    _tensor(q, (rows, cols), dtype, x.device, "q")
-    _tensor(scale, shape, torch.float32, x.device, "scale")
-    with _on(stream):
-        q = torch.empty(rows, cols, dtype=dtype, device=x.device) if q is None else q
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device) if scale is None else scale
+    dev = x.device
+    shape = (-(-cols // 128), rows) if block == "row" else (-(-rows // 128), -(-cols // 128))
+    _current(dev)
+    if q is None:
+        q = _empty((rows, cols), dtype, dev, stream)
+    else:
+        _tensor(q, (rows, cols), dtype, dev, "q")
+    if scale is None:
+        scale = _empty(shape, torch.float32, dev, stream)
+    else:
+        _tensor(scale, shape, torch.float32, dev, "scale")
     _check(lib.dora_fp8_quantize(rows, cols, code, out, _BLOCKS[block], _ptr(x), _ptr(q), _ptr(scale),
-                                 _stream_ptr(stream)))
+                                 _stream(stream, dev)))
     return q, scale
 
 
-def _product(op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype, ws, stream):
+@functools.lru_cache(maxsize=4096)
+def _desc_and_workspace(d_out: int, d_in: int, in_code: int, fp8_code: int, out_code: int, T: int, op: int):
+    """The C descriptor of these sizes and types (a byref of it) and the workspace they need."""
+    desc = Fp8Desc(d_out, d_in, in_code, fp8_code, out_code)
+    ref = ctypes.byref(desc)
+    return ref, int(load_library().dora_fp8_workspace_size(ref, T, op))
+
+
+_PLANS: dict = {}  # what a product of these shapes, types and devices needs: checked once, by signature
+
+
+def _plan(sig, op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype):
+    """Check one signature; (descriptor, workspace bytes, 8-bit operand?, shape of the result, its type, library call)."""
     torch = _torch()
     lib = load_library()
-    xn, on = ("x", "y") if op == DORA_FP8_OP_FORWARD else ("dy", "dx")
+    xn = "x" if op == DORA_FP8_OP_FORWARD else "dy"
     if x.dim() != 2 or wq.dim() != 2:
         raise ValueError(f"{xn} and wq are matrices")
     d_out, d_in = wq.shape
     K, N = (d_in, d_out) if op == DORA_FP8_OP_FORWARD else (d_out, d_in)
-    T, dev = x.shape[0], x.device
-    code = _code(x.dtype, xn, "w8")
-    up = lambda n: -(-n // 128)
-    _current(dev)
-    _tensor(x, (T, K), x.dtype, dev, xn)
+    T, dev, dtype = x.shape[0], x.device, x.dtype
+    code = _code(dtype, xn, _BOTH)
+    _tensor(x, (T, K), dtype, dev, xn)
     _tensor(wq, (d_out, d_in), torch.float8_e4m3fn, dev, "wq")
-    _tensor(w_scale, (up(d_out), up(d_in)), torch.float32, dev, "w_scale")
-    if code in (DORA_E4M3, DORA_E5M2):
-        if x_scale is None:
-            raise ValueError(f"an 8-bit {xn} needs {xn}_scale")
-        if out_dtype is None and out is None:
-            out_dtype = torch.bfloat16
-    elif x_scale is not None:
-        raise ValueError(f"{xn}_scale is for an 8-bit {xn}; a {x.dtype} one is quantised in the call")
-    _tensor(x_scale, (up(K), T), torch.float32, dev, f"{xn}_scale")
+    _tensor(w_scale, (-(-d_out // 128), -(-d_in // 128)), torch.float32, dev, "w_scale")
+    given = code in (DORA_E4M3, DORA_E5M2)
+    if given and x_scale is None:
+        raise ValueError(f"an 8-bit {xn} needs {xn}_scale")
+    if not given and x_scale is not None:
+        raise ValueError(f"{xn}_scale is for an 8-bit {xn}; a {dtype} one is quantised in the call")
     if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
-    ocode = _code(out_dtype, "out_dtype", "w")
-    _tensor(out, (T, N), out_dtype, dev, on)
-    fcode = _code(torch.float8_e4m3fn if fp8_dtype is None else fp8_dtype, "fp8_dtype", "8")
-    desc = Fp8Desc(d_out, d_in, code, fcode, ocode)
-    need = int(lib.dora_fp8_workspace_size(ctypes.byref(desc), T, op))
-    with _on(stream):
-        out = torch.empty(T, N, dtype=out_dtype, device=dev) if out is None else out
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    fn = lib.dora_fp8_forward if op == DORA_FP8_OP_FORWARD else lib.dora_fp8_backward
-    _check(fn(ctypes.byref(desc), T, _ptr(x), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
-              _stream_ptr(stream)))
+        out_dtype = out.dtype if out is not None else torch.bfloat16 if given else dtype
+    fcode = DORA_E4M3 if fp8_dtype is None else _code(fp8_dtype, "fp8_dtype", _EIGHT)
+    ref, need = _desc_and_workspace(d_out, d_in, code, fcode, _code(out_dtype, "out_dtype", _WIDE), T, op)
+    plan = (ref, need, given, (T, N), out_dtype, lib.dora_fp8_forward if op == DORA_FP8_OP_FORWARD else lib.dora_fp8_backward)
+    if len(_PLANS) > 4096:
+        _PLANS.clear()
+    _PLANS[sig] = plan
+    return plan
+
+
+def _product(op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype, ws, stream):
+    sig = (op, x.shape, x.dtype, x.device, wq.shape, wq.dtype, wq.device, w_scale.shape, w_scale.dtype, w_scale.device,
+           x_scale is None, out_dtype, fp8_dtype, None if out is None else out.dtype)
+    plan = _PLANS.get(sig) or _plan(sig, op, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype)
+    ref, need, given, shape, out_dtype, call = plan
+    dev = sig[3]
+    _current(dev)
+    if given:
+        _tensor(x_scale, (-(-x.shape[1] // 128), shape[0]), _torch().float32, dev, "x_scale" if op == DORA_FP8_OP_FORWARD else "dy_scale")
+    if out is None:
+        out = x.new_empty(shape, dtype=out_dtype) if stream is None else _empty(shape, out_dtype, dev, stream)
+    else:
+        _tensor(out, shape, out_dtype, dev, "y" if op == DORA_FP8_OP_FORWARD else "dx")
+    nbytes = need
+    if ws is not None:
+        nbytes = ws.numel() * ws.element_size()
+    elif need:
+        ws = _empty(need, _torch().uint8, dev, stream)
+    _check(call(ref, shape[0], _ptr(x), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
+                _stream(stream, dev)))
     return out
 
 
@@ -137,11 +185,10 @@ def dora_fp8_workspace_size(d_out: int, d_in: int, in_dtype, T: int, op: int, *,
                             out_dtype=None) -> int:
     """Bytes of workspace a product needs (op: DORA_FP8_OP_FORWARD or DORA_FP8_OP_BACKWARD)."""
     torch = _torch()
-    code = _code(in_dtype, "in_dtype", "w8")
+    code = _code(in_dtype, "in_dtype", _BOTH)
     out = torch.bfloat16 if out_dtype is None and code > 1 else (in_dtype if out_dtype is None else out_dtype)
-    desc = Fp8Desc(int(d_out), int(d_in), code, _code(fp8_dtype or torch.float8_e4m3fn, "fp8_dtype", "8"),
-                   _code(out, "out_dtype", "w"))
-    return int(load_library().dora_fp8_workspace_size(ctypes.byref(desc), int(T), int(op)))
+    return _desc_and_workspace(int(d_out), int(d_in), code, _code(fp8_dtype or torch.float8_e4m3fn, "fp8_dtype", _EIGHT),
+                               _code(out, "out_dtype", _WIDE), int(T), int(op))[1]
 
 
 def dora_fp8_forward(x, wq, w_scale, *, x_scale=None, out_dtype=None, fp8_dtype=None, y=None, ws=None, stream=None):

@@ -143,7 +143,7 @@ def test_products_of_given_codes(T, d_out, d_in, backward):
 
 @pytest.mark.parametrize("backward", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("T,d_out,d_in", [(1, 256, 512), (3, 1040, 272), (40, 272, 1168), (200, 528, 400), (513, 656, 784)])
+@pytest.mark.parametrize("T,d_out,d_in", [(1, 256, 512), (3, 1040, 272), (16, 400, 4624), (7, 16, 8208), (17, 144, 3600), (40, 272, 1168), (200, 528, 400), (513, 656, 784)])
 def test_products_of_wide_operands(T, d_out, d_in, dtype, backward):
     """bf16 and float32 operands, quantised in the call: equal to the product of the oracle's codes."""
     K = d_out if backward else d_in
@@ -255,7 +255,7 @@ def test_refusals_on_the_device():
     wq, ws = weight(256, 128)
     x = matrix(4, 128, torch.bfloat16)
     with pytest.raises(dw.DoraError, match="EWORKSPACE"):
-        dw.dora_fp8_forward(x, wq, ws, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        dw.dora_fp8_forward(matrix(20, 128, torch.bfloat16), wq, ws, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="contiguous"):
         dw.dora_fp8_forward(matrix(4, 256, torch.bfloat16)[:, :128], wq, ws)
     buf = torch.zeros(4 * 128 + 4, dtype=torch.bfloat16, device="cuda")

@@ -115,18 +115,19 @@ def test_fp8_descriptors(lib, bad):
 
 def test_fp8_pointers_and_workspace(lib):
     d = _desc()
-    need = lib.dora_fp8_workspace_size(ctypes.byref(d), 5, 0)
-    assert need >= 5 * 144 + 2 * 5 * 4 and need % 256 == 0
-    assert lib.dora_fp8_workspace_size(ctypes.byref(d), 5, 1) >= 5 * 256 + 2 * 5 * 4
+    assert lib.dora_fp8_workspace_size(ctypes.byref(d), 16, 0) == 0  # few tokens are quantised where they are used
+    need = lib.dora_fp8_workspace_size(ctypes.byref(d), 50, 0)
+    assert need >= 50 * 144 + 2 * 50 * 4 and need % 256 == 0
+    assert lib.dora_fp8_workspace_size(ctypes.byref(d), 50, 1) >= 50 * 256 + 2 * 50 * 4
     assert lib.dora_fp8_workspace_size(ctypes.byref(d), 5, 2) == 0
     f = lambda *a: lib.dora_fp8_forward(ctypes.byref(d), *a)
     assert f(5, None, None, FAKE, FAKE, FAKE, FAKE, need, None) == 1 and "x is NULL" in dw.dora_last_error()
     assert f(5, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, need, None) == 1 and "x_scale" in dw.dora_last_error()
     assert f(5, FAKE + 8, None, FAKE, FAKE, FAKE, FAKE, need, None) == 1 and "aligned" in dw.dora_last_error()
     assert f(5, FAKE, None, FAKE, None, FAKE, FAKE, need, None) == 1 and "w_scale" in dw.dora_last_error()
-    assert f(5, FAKE, None, FAKE, FAKE, FAKE, None, 0, None) == 3
-    assert f(5, FAKE, None, FAKE, FAKE, FAKE, FAKE, need - 1, None) == 3
-    assert f(5, FAKE, None, FAKE, FAKE, FAKE, FAKE + 16, need, None) == 1
+    assert f(50, FAKE, None, FAKE, FAKE, FAKE, None, 0, None) == 3
+    assert f(50, FAKE, None, FAKE, FAKE, FAKE, FAKE, need - 1, None) == 3
+    assert f(50, FAKE, None, FAKE, FAKE, FAKE, FAKE + 16, need, None) == 1
     assert f(-1, FAKE, None, FAKE, FAKE, FAKE, FAKE, need, None) == 1
     q = lambda *a: lib.dora_fp8_quantize(*a)
     assert q(4, 100, 0, 2, 0, FAKE, FAKE, FAKE, None) == 1 and "16" in dw.dora_last_error()
