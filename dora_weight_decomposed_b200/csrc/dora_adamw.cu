@@ -107,6 +107,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
+// a + b of two products as single additions: a packed addition would be merged with one of the packed products.
+__device__ __forceinline__ float2 add_rounded(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
@@ -415,8 +419,8 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     }
     // Each product and sum rounded by itself: the moments' stored codes then depend on the formula alone.
     g[j] = mul2(g[j], both(c.gs));
-    m[j] = add2(mul2(m[j], both(a.b1)), mul2(g[j], both(a.omb1)));
-    v[j] = add2(mul2(v[j], both(a.b2)), mul2(mul2(g[j], g[j]), both(a.omb2)));
+    m[j] = add_rounded(mul2(m[j], both(a.b1)), mul2(g[j], both(a.omb1)));
+    v[j] = add_rounded(mul2(v[j], both(a.b2)), mul2(mul2(g[j], g[j]), both(a.omb2)));
     r[j] = root(v[j]);
     if (BITS == 32) top = fmaxf(top, fmaxf(v[j].x, v[j].y));
   }
