@@ -13,10 +13,12 @@ static thread_local std::string t_last_error;
 
 void set_error(const std::string& msg) { t_last_error = msg; }
 
-static StatusReader g_more_status = nullptr;
+static StatusReader g_more_status[4];
+static int g_more = 0;
 
 bool add_status_reader(StatusReader fn) {
-  g_more_status = fn;
+  if (g_more == 4) return false;
+  g_more_status[g_more++] = fn;
   return true;
 }
 
@@ -703,10 +705,12 @@ dora_status_t dora_device_status(dora_stream_t stream, unsigned int* flags_out) 
   }
   unsigned int v = 0;
   cudaError_t e = read_and_clear_device_status(reinterpret_cast<cudaStream_t>(stream), &v);
-  unsigned int more = 0;
-  if (e == cudaSuccess && g_more_status) e = g_more_status(&more);
+  for (int i = 0; i < g_more && e == cudaSuccess; ++i) {
+    unsigned int more = 0;
+    e = g_more_status[i](&more);
+    v |= more;
+  }
   if (e != cudaSuccess) return cuda_status(e, "dora_device_status");
-  v |= more;
   *flags_out = v;
   if (v) {
     set_error("a kernel's bounded wait ran out");

@@ -80,8 +80,8 @@ dora_status_t check_sm100(const char* otherwise);
 
 // Status word written by kernels whose bounded waits ran out.
 cudaError_t read_and_clear_device_status(cudaStream_t st, unsigned int* out);
-// The 8-bit products' kernels have a status word of their own (no relocatable device code):
-// their translation unit hands its reader over when the library loads.
+// The kernels of other translation units have status words of their own (no relocatable device code):
+// each unit hands its reader over when the library loads.
 using StatusReader = cudaError_t (*)(unsigned int* out);
 bool add_status_reader(StatusReader fn);
 // One kernel whose bounded wait runs out after limit_us (failure-detection test).
