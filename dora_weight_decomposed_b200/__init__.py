@@ -47,7 +47,7 @@ EXPORTED_SYMBOLS = ("dora_workspace_size", "dora_norm", "dora_norm_noalloc", "do
                     "dora_profile_start", "dora_profile_stop", "dora_profile_count", "dora_profile_read",
                     "dora_last_error", "dora_version", "dora_fp8_quantize", "dora_fp8_workspace_size",
                     "dora_fp8_forward", "dora_fp8_backward", "dora_grad_norm_workspace_size", "dora_grad_norm",
-                    "dora_adamw")
+                    "dora_adamw", "dora_adamw_clipped")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -130,6 +130,8 @@ def load_library() -> ctypes.CDLL:
         lib.dora_grad_norm.restype = INT
         lib.dora_adamw.argtypes = [P, P, INT, P, P, P]
         lib.dora_adamw.restype = INT
+        lib.dora_adamw_clipped.argtypes = [P, P, INT, P, ctypes.c_float, P, P, SZ, P]
+        lib.dora_adamw_clipped.restype = INT
         lib.dora_last_error.argtypes = []
         lib.dora_last_error.restype = ctypes.c_char_p
         lib.dora_version.argtypes = []

@@ -143,9 +143,10 @@ class DoraAdamW:
         self._tensors = (AdamwTensor * n)(*rows)
         self._n, self._device, self._keep = n, device, (params, grads)
         self._ref, self._control_ptr = ctypes.byref(self._desc), self._control.data_ptr()
-        # What a clipped step keeps between its kernels.
-        self._scale = torch.zeros((), **f32)
-        self._ws = torch.empty(int(load_library().dora_grad_norm_workspace_size(n)), dtype=torch.uint8, device=device)
+        # The partial sums that a clipped step keeps between its kernels.
+        self._ws_bytes = int(load_library().dora_grad_norm_workspace_size(n))
+        self._ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=device)
+        self._ws_ptr = self._ws.data_ptr()
 
     def set_lr(self, lr: float) -> None:
         """The learning rate of the steps queued from now on (written on the current stream)."""
@@ -171,18 +172,20 @@ class DoraAdamW:
         torch = _torch()
         device = self._device
         _current(device)
-        norm = None
+        lib = load_library()
         if max_norm is not None:
             if grad_scale is not None:
                 raise ValueError("give max_norm or grad_scale, not both")
-            norm, grad_scale = _empty((), torch.float32, device, stream), self._scale
-            _grad_norm(self._grads, self._n, float(max_norm), norm, grad_scale, self._ws, device, stream)
-        elif grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or
-                                         grad_scale.device != device):
+            norm = _empty((), torch.float32, device, stream)
+            _check(lib.dora_adamw_clipped(self._ref, self._tensors, self._n, self._control_ptr, max_norm, norm.data_ptr(),
+                                          self._ws_ptr, self._ws_bytes, _stream(stream, device)))
+            return norm
+        if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or
+                                       grad_scale.device != device):
             raise ValueError(f"grad_scale must be one float32 value on {device}")
-        _check(load_library().dora_adamw(self._ref, self._tensors, self._n, self._control_ptr, _ptr(grad_scale),
-                                         _stream(stream, device)))
-        return norm
+        _check(lib.dora_adamw(self._ref, self._tensors, self._n, self._control_ptr, _ptr(grad_scale),
+                              _stream(stream, device)))
+        return None
 
     def state_dict(self) -> dict:
         """The live state: flat moments (8 bits: codes and scales), the master copy, the step count (int64 tensor)."""

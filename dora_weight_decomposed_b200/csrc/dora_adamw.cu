@@ -159,28 +159,31 @@ __device__ __forceinline__ void values(const Raw8& r, int fp32, float2 (&v)[4]) 
   }
 }
 
+template <bool WHOLE = false>
 __device__ __forceinline__ void store8(void* base, int fp32, int vec, int64_t i, int64_t n, const float2 (&v)[4]) {
-  if (vec && i + 8 <= n) {
-    if (fp32) {
-      float4* p = reinterpret_cast<float4*>((float*)base + i);
-      p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    } else {
-      __nv_bfloat162 h[4];
+  if constexpr (!WHOLE) {
+    if (!vec || i + 8 > n) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(v[j]);
-      *reinterpret_cast<uint4*>((__nv_bfloat16*)base + i) = *reinterpret_cast<const uint4*>(h);
+      for (int j = 0; j < 8; ++j) {
+        if (i + j >= n) return;
+        const float x = (j & 1) ? v[j / 2].y : v[j / 2].x;
+        if (fp32)
+          ((float*)base)[i + j] = x;
+        else
+          ((__nv_bfloat16*)base)[i + j] = __float2bfloat16_rn(x);
+      }
+      return;
     }
-    return;
   }
+  if (fp32) {
+    float4* p = reinterpret_cast<float4*>((float*)base + i);
+    p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  } else {
+    __nv_bfloat162 h[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (i + j >= n) return;
-    const float x = (j & 1) ? v[j / 2].y : v[j / 2].x;
-    if (fp32)
-      ((float*)base)[i + j] = x;
-    else
-      ((__nv_bfloat16*)base)[i + j] = __float2bfloat16_rn(x);
+    for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(v[j]);
+    *reinterpret_cast<uint4*>((__nv_bfloat16*)base + i) = *reinterpret_cast<const uint4*>(h);
   }
 }
 
@@ -207,14 +210,17 @@ __device__ __forceinline__ void code_values(uint2 u, float2 (&v)[4]) {
   }
 }
 
+template <bool WHOLE>
 __device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, int64_t n, uint2 u) {
-  if (i + 8 <= n) {
-    *reinterpret_cast<uint2*>(base + i) = u;
-  } else {
+  if constexpr (!WHOLE) {
+    if (i + 8 > n) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < n) base[i + j] = (uint8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
+      for (int j = 0; j < 8; ++j)
+        if (i + j < n) base[i + j] = (uint8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
+      return;
+    }
   }
+  *reinterpret_cast<uint2*>(base + i) = u;
 }
 
 // The chunks [first, last) of one CTA: contiguous, so that the tensor they lie in is found once and then followed.
@@ -281,24 +287,35 @@ __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __gri
   }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double* __restrict__ part, int n, float max_norm,
-                                                                   float* __restrict__ norm, float* __restrict__ scale) {
+// sqrt of the sum of the partial sums (the whole block takes part; every block gets the same value), and the scale.
+struct NormScale {
+  double norm;
+  float scale;
+};
+__device__ __forceinline__ NormScale norm_and_scale(const double* part, int n, float max_norm) {
   __shared__ double red[kThreads / 32];
-  pdl_trigger();
-  pdl_wait();
   double sum = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) sum += part[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+  s = sqrt(s);
+  const double c = (double)max_norm / (s + 1e-6);
+  return {s, !isfinite(s) ? __uint_as_float(0x7fffffffu) : (float)(c < 1.0 ? c : 1.0)};
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double* __restrict__ part, int n, float max_norm,
+                                                                   float* __restrict__ norm, float* __restrict__ scale) {
+  pdl_trigger();
+  pdl_wait();
+  const NormScale r = norm_and_scale(part, n, max_norm);
   if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-    s = sqrt(s);
-    *norm = (float)s;
-    const double c = (double)max_norm / (s + 1e-6);
-    *scale = !isfinite(s) ? __uint_as_float(0x7fffffffu) : (float)(c < 1.0 ? c : 1.0);
+    *norm = (float)r.norm;
+    *scale = r.scale;
   }
 }
 
@@ -309,6 +326,12 @@ struct AdamArgs {
   float ln_b1, ln_b2;
   float eps;
   uint32_t seed;
+  // Clipping within the step: the partial sums of grad_norm_partial_kernel, which every CTA adds up for itself in the
+  // same order (a few KB from L2, where a kernel of its own between the two would cost its launch).
+  const double* part;
+  int parts;
+  float max_norm;
+  float* norm;
 };
 
 // Integer hash: two rounds of xor-shift and an odd multiplier (the leading
@@ -410,8 +433,9 @@ __device__ __forceinline__ void load_elements(const AdamEntry& e, int64_t i, Ele
   }
 }
 
-// The update of elements i .. i + 7 of tensor e by one thread; the warp's lanes hold consecutive ones.
-template <int BITS>
+// The update of elements i .. i + 7 of tensor e by one thread; the warp's lanes hold consecutive ones. WHOLE: the
+// elements lie in a whole chunk of an aligned tensor.
+template <int BITS, bool WHOLE>
 __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, const StepScalars& c, int64_t i,
                                        const Elements<BITS>& x) {
   const int64_t n = e.n;
@@ -457,11 +481,11 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     const float2 den = fma2(r[j], both(c.rbc2), both(a.eps));
     p[j] = fma2(mul2(m[j], both(-c.lr1)), make_float2(reciprocal(den.x), reciprocal(den.y)), mul2(p[j], keep));
   }
-  if (e.master) store8(e.master, 1, 1, i, n, p);
-  store8(e.p, e.p_fp32, e.p_vec, i, n, p);
+  if (e.master) store8<WHOLE>(e.master, 1, 1, i, n, p);
+  store8<WHOLE>(e.p, e.p_fp32, e.p_vec, i, n, p);
   if (BITS == 32) {
-    store8(e.avg, 1, 1, i, n, m);
-    store8(e.sq, 1, 1, i, n, v);
+    store8<WHOLE>(e.avg, 1, 1, i, n, m);
+    store8<WHOLE>(e.sq, 1, 1, i, n, v);
     return;
   }
   uint2 cm = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), cr = cm;  // NaN codes
@@ -485,9 +509,9 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     cm = make_uint2(top_bytes(zm[0], zm[1], zm[2], zm[3]), top_bytes(zm[4], zm[5], zm[6], zm[7]));
     cr = make_uint2(top_bytes(zr[0], zr[1], zr[2], zr[3]), top_bytes(zr[4], zr[5], zr[6], zr[7]));
   }
-  store_codes((uint8_t*)e.avg, i, n, cm);
-  store_codes((uint8_t*)e.sq, i, n, cr);
-  if ((threadIdx.x & 15) == 0 && i < n) {
+  store_codes<WHOLE>((uint8_t*)e.avg, i, n, cm);
+  store_codes<WHOLE>((uint8_t*)e.sq, i, n, cr);
+  if ((threadIdx.x & 15) == 0 && (WHOLE || i < n)) {
     e.savg[i >> 7] = sm;
     e.ssq[i >> 7] = sr;
   }
@@ -570,10 +594,11 @@ __device__ __forceinline__ void update_range_staged(const AdamTable<MAX>& t, con
         x.cv = reinterpret_cast<const uint2*>(s.cv)[threadIdx.x];
         x.sm = s.sm[threadIdx.x >> 4];
         x.sr = s.sr[threadIdx.x >> 4];
+        update<8, true>(e, a, sc, i, x);
       } else {
         load_elements<8>(e, i, x);
+        update<8, false>(e, a, sc, i, x);
       }
-      update<8>(e, a, sc, i, x);
     }
     k = kn;
     __syncthreads();  // the stage has been read
@@ -594,6 +619,11 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   StepScalars sc;
   sc.lr = control->lr;
   sc.gs = grad_scale ? *grad_scale : 1.0f;
+  if (a.part) {
+    const NormScale r = norm_and_scale(a.part, a.parts, a.max_norm);
+    sc.gs = r.scale;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)r.norm;
+  }
   const bool run = isfinite(sc.gs);
   const Range range = cta_range(t.chunks);
   if (run && range.first < range.last) {
@@ -612,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
         for (; c < end; ++c, i += kChunk) {
           Elements<BITS> x;
           load_elements<BITS>(e, i, x);
-          update<BITS>(e, a, sc, i, x);
+          update<BITS, false>(e, a, sc, i, x);
         }
       }
     }
@@ -658,13 +688,29 @@ bool check_nth(const void* p, const char* name, int i, size_t align) {
 constexpr int64_t kMaxNumel = int64_t(1) << 40;
 
 // One launch over the tensors from i on, as many as the table holds.
-template <int MAX>
-cudaError_t launch_norm(const dora_grad_t* grads, int n_tensors, int most, double* part, int& parts, int& i,
+template <int MAX, class Grads>
+cudaError_t launch_norm(const Grads& grads, int n_tensors, int most, double* part, int& parts, int& i,
+                        cudaStream_t st);
+
+// The partial sums of all tensors (grads(i) is the i-th), `parts` of them.
+template <class Grads>
+cudaError_t norm_partials(const Grads& grads, int n_tensors, double* part, int& parts, cudaStream_t st) {
+  const int most = std::min(kNormBlocksMax, device_sm_count() * kNormBlocksPerSM);
+  cudaError_t e = cudaSuccess;
+  parts = 0;
+  for (int i = 0; i < n_tensors && e == cudaSuccess;)
+    e = n_tensors <= kFew ? launch_norm<kFew>(grads, n_tensors, most, part, parts, i, st)
+                          : launch_norm<kMaxGrads>(grads, n_tensors, most, part, parts, i, st);
+  return e;
+}
+
+template <int MAX, class Grads>
+cudaError_t launch_norm(const Grads& grads, int n_tensors, int most, double* part, int& parts, int& i,
                         cudaStream_t st) {
   GradTable<MAX> t;
   t.n = t.chunks = 0;
   for (; i < n_tensors && t.n < MAX; ++i) {
-    const dora_grad_t& g = grads[i];
+    const dora_grad_t g = grads(i);
     if (g.numel == 0) continue;
     t.first[t.n] = t.chunks;
     t.e[t.n++] = {g.grad, g.numel, g.dtype == DORA_FP32, aligned16(g.grad)};
@@ -705,48 +751,25 @@ cudaError_t launch_adamw(const AdamArgs& a, const dora_adamw_tensor_t* tensors, 
 
 using namespace dora;
 
-extern "C" {
-
-size_t dora_grad_norm_workspace_size(int n_tensors) {
-  if (n_tensors < 0) return 0;
-  return (size_t)std::max<int64_t>(1, cdiv(n_tensors, kMaxGrads)) * kNormBlocksMax * sizeof(double);
-}
-
-dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, float max_norm, float* norm, float* scale,
-                             void* ws, size_t ws_bytes, dora_stream_t stream) {
-  if (n_tensors < 0 || (n_tensors > 0 && !grads)) return set_error("grads is NULL or n_tensors negative"), DORA_EINVAL;
+template <class Grads>
+static dora_status_t check_grads(const Grads& grads, int n_tensors, float max_norm, const void* ws, size_t ws_bytes) {
   if (!(max_norm > 0.f)) return set_error("max_norm must be > 0"), DORA_EINVAL;
-  if (!check_ptr(norm, "norm", 4) || !check_ptr(scale, "scale", 4)) return DORA_EINVAL;
   int64_t total = 0;
   for (int i = 0; i < n_tensors; ++i) {
-    const dora_grad_t& g = grads[i];
+    const dora_grad_t g = grads(i);
     if (g.numel < 0 || g.numel > kMaxNumel) return set_error(nth("numel out of range", i)), DORA_EINVAL;
     if (!is_wide(g.dtype)) return set_error(nth("dtype is not DORA_BF16 or DORA_FP32", i)), DORA_EINVAL;
     if (g.numel > 0 && !check_nth(g.grad, "grad", i, width(g.dtype))) return DORA_EINVAL;
     total += cdiv(g.numel, kChunk);
   }
   if (total > INT32_MAX) return set_error("too many elements for one call"), DORA_EINVAL;
-  dora_status_t s = check_ws_bytes(dora_grad_norm_workspace_size(n_tensors), ws, ws_bytes);
-  if (s != DORA_OK) return s;
-  if ((s = check_sm100("dora_grad_norm needs an sm_100 (B200) device")) != DORA_OK) return s;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  double* part = reinterpret_cast<double*>(ws);
-  const int most = std::min(kNormBlocksMax, device_sm_count() * kNormBlocksPerSM);
-  int parts = 0;
-  cudaError_t e = cudaSuccess;
-  for (int i = 0; i < n_tensors && e == cudaSuccess;)
-    e = n_tensors <= kFew ? launch_norm<kFew>(grads, n_tensors, most, part, parts, i, st)
-                          : launch_norm<kMaxGrads>(grads, n_tensors, most, part, parts, i, st);
-  if (e == cudaSuccess) {
-    ProfRange pr("grad_norm_final", st);
-    e = launch_pdl(grad_norm_final_kernel, dim3(1), dim3(kThreads), 0, st, (const double*)part, parts, max_norm, norm,
-                   scale);
-  }
-  return cuda_status(e, "dora_grad_norm");
+  return check_ws_bytes(dora_grad_norm_workspace_size(n_tensors), ws, ws_bytes);
 }
 
-dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
-                         dora_adamw_control_t* control, const float* grad_scale, dora_stream_t stream) {
+// norm: clip by the global norm of the tensors' gradients, written there; else grad_scale (or 1).
+static dora_status_t adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
+                           dora_adamw_control_t* control, const float* grad_scale, float max_norm, float* norm, void* ws,
+                           size_t ws_bytes, dora_stream_t stream) {
   if (!desc) return set_error("desc is NULL"), DORA_EINVAL;
   if (!(desc->beta1 >= 0.0 && desc->beta1 < 1.0 && desc->beta2 >= 0.0 && desc->beta2 < 1.0))
     return set_error("beta1 and beta2 must be in [0, 1)"), DORA_EINVAL;
@@ -772,12 +795,21 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
       return DORA_EINVAL;
   }
   if (total > INT32_MAX) return set_error("too many elements for one call"), DORA_EINVAL;
-  const dora_status_t s = check_sm100("dora_adamw needs an sm_100 (B200) device");
-  if (s != DORA_OK) return s;
+  const auto nth_grad = [=](int i) { return dora_grad_t{tensors[i].grad, tensors[i].numel, tensors[i].grad_dtype}; };
+  dora_status_t s;
+  if (norm && (s = check_grads(nth_grad, n_tensors, max_norm, ws, ws_bytes)) != DORA_OK) return s;
+  if ((s = check_sm100("dora_adamw needs an sm_100 (B200) device")) != DORA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = norm ? reinterpret_cast<double*>(ws) : nullptr;
+  int parts = 0;
+  if (norm) {
+    const cudaError_t e = norm_partials(nth_grad, n_tensors, part, parts, st);
+    if (e != cudaSuccess) return cuda_status(e, "dora_adamw_clipped");
+  }
   const AdamArgs a{(float)desc->beta1,          (float)(1.0 - desc->beta1),   (float)desc->beta2,
                    (float)(1.0 - desc->beta2),  (float)std::log(desc->beta1), (float)std::log(desc->beta2),
-                   desc->eps,                   desc->seed};
+                   desc->eps,                   desc->seed,                   part,
+                   parts,                       max_norm,                     norm};
   const bool few = n_tensors <= kFew;
   cudaError_t e;
   int i = 0;
@@ -788,6 +820,45 @@ dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_
                      : launch_adamw<32, kMaxAdam>(a, tensors, n_tensors, i, control, grad_scale, st));
   } while (i < n_tensors && e == cudaSuccess);
   return cuda_status(e, "dora_adamw");
+}
+
+extern "C" {
+
+size_t dora_grad_norm_workspace_size(int n_tensors) {
+  if (n_tensors < 0) return 0;
+  return (size_t)std::max<int64_t>(1, cdiv(n_tensors, kMaxGrads)) * kNormBlocksMax * sizeof(double);
+}
+
+dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, float max_norm, float* norm, float* scale,
+                             void* ws, size_t ws_bytes, dora_stream_t stream) {
+  if (!check_ptr(norm, "norm", 4) || !check_ptr(scale, "scale", 4)) return DORA_EINVAL;
+  if (n_tensors < 0 || (n_tensors > 0 && !grads)) return set_error("grads is NULL or n_tensors negative"), DORA_EINVAL;
+  const auto nth_grad = [=](int i) { return grads[i]; };
+  dora_status_t s = check_grads(nth_grad, n_tensors, max_norm, ws, ws_bytes);
+  if (s != DORA_OK) return s;
+  if ((s = check_sm100("dora_grad_norm needs an sm_100 (B200) device")) != DORA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = reinterpret_cast<double*>(ws);
+  int parts = 0;
+  cudaError_t e = norm_partials(nth_grad, n_tensors, part, parts, st);
+  if (e == cudaSuccess) {
+    ProfRange pr("grad_norm_final", st);
+    e = launch_pdl(grad_norm_final_kernel, dim3(1), dim3(kThreads), 0, st, (const double*)part, parts, max_norm, norm,
+                   scale);
+  }
+  return cuda_status(e, "dora_grad_norm");
+}
+
+dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
+                         dora_adamw_control_t* control, const float* grad_scale, dora_stream_t stream) {
+  return adamw(desc, tensors, n_tensors, control, grad_scale, 1.f, nullptr, nullptr, 0, stream);
+}
+
+dora_status_t dora_adamw_clipped(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
+                                 dora_adamw_control_t* control, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                                 dora_stream_t stream) {
+  if (!check_ptr(norm, "norm", 4)) return DORA_EINVAL;
+  return adamw(desc, tensors, n_tensors, control, nullptr, max_norm, norm, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -323,6 +323,10 @@ DORA_API dora_status_t dora_fp8_backward(const dora_fp8_desc_t* desc, int64_t T,
  *   tensors and dora_grad_t arrays are host memory, read before the call
  *   returns. exp_avg, exp_avg_sq and master are 16-byte aligned, param and
  *   grad to their element size. Tensors must not overlap. No workspace.
+ *
+ * dora_adamw_clipped: the same step with grad_scale = the scale of
+ *   dora_grad_norm over the tensors' gradients (bit for bit), in one launch
+ *   less; norm receives their norm. Workspace as dora_grad_norm.
  */
 typedef struct {
   const void* grad;
@@ -363,6 +367,9 @@ DORA_API dora_status_t dora_grad_norm(const dora_grad_t* grads, int n_tensors, f
                                       float* scale, void* ws, size_t ws_bytes, dora_stream_t stream);
 DORA_API dora_status_t dora_adamw(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors, int n_tensors,
                                   dora_adamw_control_t* control, const float* grad_scale, dora_stream_t stream);
+DORA_API dora_status_t dora_adamw_clipped(const dora_adamw_desc_t* desc, const dora_adamw_tensor_t* tensors,
+                                          int n_tensors, dora_adamw_control_t* control, float max_norm, float* norm,
+                                          void* ws, size_t ws_bytes, dora_stream_t stream);
 
 /*
  * dora_device_status -- synchronise `stream`, then read and clear the library's

@@ -226,6 +226,24 @@ def test_graph_replays_further_steps(bits):
     assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
+@pytest.mark.parametrize("sizes", [[3000, 50], [(i * 53) % 900 + 1 for i in range(800)]])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_clipping_in_the_step_and_before_it_agree(sizes, bits):
+    """step(max_norm=) gives the bits of grad_norm(max_norm) followed by step(grad_scale=)."""
+    res = []
+    for fused in (True, False):
+        params, grads = draw(sizes, (BF, F32), seed=30), draw(sizes, (BF,), seed=31, std=3.0)
+        opt = dw.DoraAdamW(params, grads, lr=LR, state_bits=bits, seed=2)
+        for _ in range(2):
+            if fused:
+                norm = opt.step(max_norm=0.7)
+            else:
+                norm, scale = opt.grad_norm(0.7)
+                opt.step(grad_scale=scale)
+        res.append([norm] + params + [v.clone().view(torch.uint8) for k, v in opt.state_dict().items() if k != "step"])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_saved_state_continues():
     params, grads = draw([3000, 50], (BF,), seed=13), draw([3000, 50], (BF,), seed=14)
     a = dw.DoraAdamW(params, grads, lr=LR, state_bits=8, master=True, seed=9)

@@ -178,5 +178,10 @@ def test_adamw_and_norm_pointers(lib):
     assert lib.dora_grad_norm(g, 1, 0.0, FAKE, FAKE, FAKE, need, None) == 1
     assert lib.dora_grad_norm(g, 1, float("nan"), FAKE, FAKE, FAKE, need, None) == 1
     assert lib.dora_grad_norm(g, 1, 1.0, None, FAKE, FAKE, need, None) == 1
+    c = lambda *a: lib.dora_adamw_clipped(ctypes.byref(d), t, 1, FAKE, *a, None)
+    assert c(1.0, None, FAKE, need) == 1 and "norm" in dw.dora_last_error()
+    assert c(-1.0, FAKE, FAKE, need) == 1 and "max_norm" in dw.dora_last_error()
+    assert c(1.0, FAKE, FAKE, need - 1) == 3
+    assert c(1.0, FAKE, None, need) == 3
     bad = (da.GradEntry * 1)(da.GradEntry(FAKE + 1, 10, 0))
     assert lib.dora_grad_norm(bad, 1, 1.0, FAKE, FAKE, FAKE, need, None) == 1
