@@ -19,11 +19,20 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // 1 x 128 blocks. It lets the next grid start only once all work before it is done, so that a product which
 // follows it may read the weight at once. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
 // in flight; the CTA's eight warps take neighbouring column blocks. Bound by HBM.
+// ws, flag: in front of a product, the first CTA also says whether all n_ws scales of the weight are powers of two.
 template <class T, bool E5M2>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
-                                                                uint8_t* __restrict__ q, float* __restrict__ scale) {
+                                                                uint8_t* __restrict__ q, float* __restrict__ scale,
+                                                                const float* __restrict__ ws, int n_ws, int* flag) {
   pdl_wait();
   pdl_trigger();
+  if (flag && blockIdx.x == 0 && blockIdx.y == 0) {
+    bool all = true;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n_ws; i += 256) all = all && is_power(ws[i]);
+    all = __syncthreads_and(all);
+    if (threadIdx.x == 0) *flag = all ? 1 : 0;
+  }
   const int kb = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (kb >= nkb) return;
   const int sub = threadIdx.x & 15, h = (threadIdx.x >> 4) & 1;
@@ -92,24 +101,48 @@ __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __rest
   if (threadIdx.x == 0) scale[blockIdx.x] = s.scale;
 }
 
+// One flag per CTA: whether its part of x's scales (a non-finite one counts, see is_power_or_bad) and of the weight's
+// are powers of two. For a product whose operand comes in codes.
+__global__ void __launch_bounds__(256) fp8_check_scales_kernel(const float* __restrict__ xs, long long n_xs,
+                                                               const float* __restrict__ ws, int n_ws, int* flags) {
+  pdl_wait();
+  pdl_trigger();
+  bool all = true;
+  const long long step = (long long)gridDim.x * 256;
+#pragma unroll 4
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n_xs; i += step) all = all && is_power_or_bad(xs[i]);
+#pragma unroll 4
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n_ws; i += step) all = all && is_power(ws[i]);
+  all = __syncthreads_and(all);
+  if (threadIdx.x == 0) flags[blockIdx.x] = all ? 1 : 0;
+}
+
+// The weight's scales that a product wants looked at on the way (none for the quantiser alone).
+struct WeightCheck {
+  const float* ws = nullptr;
+  int n = 0;
+  int* flag = nullptr;
+};
+
 template <class T, bool E5M2>
-cudaError_t quantize_t(int64_t rows, int64_t cols, bool tiles, const void* x, void* q, float* scale, cudaStream_t st) {
+cudaError_t quantize_t(int64_t rows, int64_t cols, bool tiles, const void* x, void* q, float* scale, const WeightCheck& wc,
+                       cudaStream_t st) {
   const int nkb = (int)cdiv(cols, 128);
   ProfRange pr(tiles ? "fp8_quantize_tiles" : "fp8_quantize_rows", st);
   if (tiles)
     return launch_pdl(fp8_quantize_tiles_kernel<T, E5M2>, dim3((unsigned)(cdiv(rows, 128) * nkb)), dim3(256), 0, st,
                       (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
   return launch_pdl(fp8_quantize_rows_kernel<T, E5M2>, dim3((unsigned)cdiv(rows, 16), (unsigned)cdiv(nkb, 8)), dim3(256),
-                    0, st, (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
+                    0, st, (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale, wc.ws, wc.n, wc.flag);
 }
 
 cudaError_t quantize(int64_t rows, int64_t cols, dora_dtype_t in, dora_dtype_t fp8, bool tiles, const void* x, void* q,
-                     float* scale, cudaStream_t st) {
+                     float* scale, const WeightCheck& wc, cudaStream_t st) {
   if (in == DORA_BF16)
-    return fp8 == DORA_E5M2 ? quantize_t<__nv_bfloat16, true>(rows, cols, tiles, x, q, scale, st)
-                            : quantize_t<__nv_bfloat16, false>(rows, cols, tiles, x, q, scale, st);
-  return fp8 == DORA_E5M2 ? quantize_t<float, true>(rows, cols, tiles, x, q, scale, st)
-                          : quantize_t<float, false>(rows, cols, tiles, x, q, scale, st);
+    return fp8 == DORA_E5M2 ? quantize_t<__nv_bfloat16, true>(rows, cols, tiles, x, q, scale, wc, st)
+                            : quantize_t<__nv_bfloat16, false>(rows, cols, tiles, x, q, scale, wc, st);
+  return fp8 == DORA_E5M2 ? quantize_t<float, true>(rows, cols, tiles, x, q, scale, wc, st)
+                          : quantize_t<float, false>(rows, cols, tiles, x, q, scale, wc, st);
 }
 
 // ------------------------------------------------------------------ products
@@ -243,8 +276,8 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
 
 // What a call keeps in its workspace (the quantised operand and its scales), unless the kernel quantises it itself.
 struct Fp8Plan {
-  bool own_x = false;
-  size_t off_q = 0, off_s = 0, total = 0;
+  bool own_x = false, narrow = true;
+  size_t off_q = 0, off_s = 0, off_flags = 0, total = 0;
 };
 
 bool is_fp8(dora_dtype_t t) { return t == DORA_E4M3 || t == DORA_E5M2; }
@@ -254,7 +287,10 @@ Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
   Fp8Plan p;
   const bool back = op == DORA_FP8_OP_BACKWARD, bf16 = d.in_dtype == DORA_BF16;
   const int64_t K = back ? d.d_out : d.d_in, N = back ? d.d_in : d.d_out, nkb = cdiv(K, 128);
-  if (is_fp8(d.in_dtype) || T == 0) return p;
+  if (T == 0) return p;
+  p.narrow = T <= 128;
+  if (!p.narrow) p.total = kF8MaxFlags * sizeof(int);  // the pair kernel's flags
+  if (is_fp8(d.in_dtype)) return p;
   if (T <= 16 && nkb <= 8 * Fp8Narrow<16>::STAGES) {
     const int64_t tiles = cdiv(N, 128);
     const int cs = back ? (bf16 ? narrow_splits<16, true, __nv_bfloat16>(tiles, nkb) : narrow_splits<16, true, float>(tiles, nkb))
@@ -262,7 +298,8 @@ Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
     p.own_x = cdiv(nkb, cs) <= Fp8Narrow<16>::STAGES;
   }
   if (p.own_x) return p;
-  p.off_s = align256((size_t)T * K);
+  p.off_q = p.total;
+  p.off_s = p.off_q + align256((size_t)T * K);
   p.total = p.off_s + align256((size_t)T * nkb * 4);
   return p;
 }
@@ -300,16 +337,27 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   const int64_t K = backward ? desc->d_out : desc->d_in, N = backward ? desc->d_in : desc->d_out;
   const dora_dtype_t type = given ? desc->in_dtype : desc->fp8_dtype;
   const void* xq = x;
+  const int n_ws = (int)(cdiv(desc->d_out, 128) * cdiv(desc->d_in, 128));
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  int* flags = p.narrow ? nullptr : reinterpret_cast<int*>(w + p.off_flags);
+  int n_flags = 1;
   if (!given && !p.own_x) {
-    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-    const cudaError_t e = quantize(T, K, desc->in_dtype, type, false, x, w + p.off_q, reinterpret_cast<float*>(w + p.off_s), st);
+    const cudaError_t e = quantize(T, K, desc->in_dtype, type, false, x, w + p.off_q, reinterpret_cast<float*>(w + p.off_s),
+                                   WeightCheck{w_scale, n_ws, flags}, st);
     if (e != cudaSuccess) return cuda_status(e, where);
     xq = w + p.off_q;
     x_scale = reinterpret_cast<const float*>(w + p.off_s);
+  } else if (flags) {
+    const long long n_xs = (long long)T * cdiv(K, 128);
+    n_flags = (int)std::min<long long>(kF8MaxFlags, cdiv(n_xs, 1024));
+    ProfRange pr("fp8_check_scales", st);
+    const cudaError_t e = launch_pdl(fp8_check_scales_kernel, dim3((unsigned)n_flags), dim3(256), 0, st, x_scale, n_xs, w_scale,
+                                     n_ws, flags);
+    if (e != cudaSuccess) return cuda_status(e, where);
   }
   const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
   Fp8Geom g{x, (int)K, x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
-            desc->out_dtype == DORA_FP32, type == DORA_E5M2};
+            desc->out_dtype == DORA_FP32, type == DORA_E5M2, flags, flags ? n_flags : 0};
   CUtensorMap tx, tw;
   cudaError_t e = make_map_2d(&tw, W, desc->d_out, desc->d_in, 1, 128);
   if (e != cudaSuccess) return cuda_status(e, where);
@@ -323,7 +371,7 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
     return cuda_status(e, where);
   }
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  const bool narrow = T <= 128;
+  const bool narrow = p.narrow;
   e = make_map_2d(&tx, xq, T, K, 1, narrow ? nt : 128);
   if (e == cudaSuccess) {
     if (narrow)
@@ -368,7 +416,7 @@ dora_status_t dora_fp8_quantize(int64_t rows, int64_t cols, dora_dtype_t in_dtyp
   if (!check_ptr(x, "x", 16) || !check_ptr(q, "q", 16) || !check_ptr(scale, "scale", 4)) return DORA_EINVAL;
   const dora_status_t s = check_sm100("the 8-bit calls need an sm_100 (B200) device");
   if (s != DORA_OK) return s;
-  return cuda_status(quantize(rows, cols, in_dtype, fp8_dtype, block == DORA_FP8_TILES, x, q, scale,
+  return cuda_status(quantize(rows, cols, in_dtype, fp8_dtype, block == DORA_FP8_TILES, x, q, scale, WeightCheck{},
                               reinterpret_cast<cudaStream_t>(stream)),
                      "dora_fp8_quantize");
 }

@@ -117,7 +117,20 @@ struct Fp8Geom {
   int ws_n, ws_k;
   int out_fp32;
   int a_e5m2;
+  // Whether every scale is a power of two: n_flags words, each nonzero if its part of them is (pair kernel).
+  const int* flags;
+  int n_flags;
 };
+
+// A scale that the tensor cores can apply: a positive normal power of two; or a non-finite scale of x, which stands for
+// NaN there and makes its row's results NaN either way.
+__device__ __forceinline__ bool is_power(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x807fffffu) == 0 && u != 0 && u < 0x7f800000u;
+}
+__device__ __forceinline__ bool is_power_or_bad(float s) { return is_power(s) || !(fabsf(s) < __uint_as_float(0x7f800000u)); }
+
+constexpr int kF8MaxFlags = 64;
 
 // Eight 16-byte pieces of one row of a box (32 rows of 128 bytes, 128-byte swizzle), as a tiled store reads it.
 __device__ __forceinline__ void fp8_stage_row(uint8_t* box, int lane, const uint4 (&p)[8]) {
@@ -433,9 +446,14 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 // the weight tile's 256, so that per k-block (512 clocks of MMA per SM) only 32 KB
 // come in per SM. TMEM (512 columns) holds two accumulators of 256. Eight
 // epilogue warps fold: warp w reads TMEM lanes 32 (w % 4) .. + 31 and
-// half of the columns, 128 fp32 sums per thread, so that each scheduler issues
-// about half as many instructions as a k-block of MMAs takes clocks. Tiles
-// are walked persistently; the MMAs of the next tile start while this one is stored.
+// half of the columns, 128 fp32 sums per thread. Tiles are walked persistently; the MMAs of the next tile start while
+// this one is stored.
+//
+// Folding and MMAs take about 750 and 700 clocks per k-block and meet at the two accumulators, so the sum of a
+// k-block costs 955. When every scale is a power of two (as dora_fp8_quantize makes them; `flags` says so) the tensor
+// cores apply the scales themselves (kind::mxf8f6f4): four warps write each k-block's scales into TMEM as exponent
+// bytes, one accumulator holds the tile's whole sum, and the folding warps only store it. The same values come out of
+// both up to the order of fp32 additions.
 constexpr int kF8FoldWarps = 8;
 constexpr int kF8PairThreads = 128 + 32 * kF8FoldWarps;
 // The block launches with 384 x 168 registers, the most that 384 threads can have; the folding warps take 216 each and
@@ -470,7 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;  // [2] accumulator complete
   uint64_t* acce = accf + 2;        // [2] accumulator folded by both CTAs, used in the leader
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+  uint64_t* sff = acce + 2;         // [STAGES] a k-block's scales are in TMEM of both CTAs, used in the leader
+  uint64_t* sume = sff + STAGES;    // the tile's sum has been read by both CTAs, used in the leader
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sume + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -483,7 +503,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sff[s], 8);
     }
+    mbar_init(sume, 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
       mbar_init(&acce[b], 2 * kF8FoldWarps);
@@ -504,6 +526,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
   pdl_wait();
+  bool mx = true;
+  for (int f = lane; f < g.n_flags; f += 32) mx = mx && g.flags[f] != 0;
+  mx = __all_sync(0xffffffffu, mx);
+  constexpr uint32_t SCALE_COL = 256;  // of stage s: 4 columns of x's scales and 8 of the weight's at 256 + 16 s
 
   if (warp < 4) {
     setmaxnreg_dec<kF8OtherRegs>();
@@ -537,10 +563,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
           mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, kWaitLimitNs / 16);
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_fp8_f32(256, 256, g.a_e5m2 != 0, false, B_MN);
+      const uint32_t idesc = mx ? idesc_mxfp8(256, 256, g.a_e5m2 != 0, false, B_MN)
+                                : idesc_fp8_f32(256, 256, g.a_e5m2 != 0, false, B_MN);
       constexpr uint32_t b_kstep = B_MN ? 32u * 128u : 32u;
       int it = 0;
       bool ok = true;
+      if (mx) {
+        int j = 0;
+#pragma unroll 1
+        for (int t = pair; t < tiles && ok; t += npairs, ++j) {
+          if (!mbar_wait(sume, ((uint32_t)j & 1u) ^ 1u)) break;
+#pragma unroll 1
+          for (int kb = 0; kb < g.nkb; ++kb, ++it) {
+            const int s = it % STAGES;
+            const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
+            if (!mbar_wait(&sff[s], ph) || !mbar_wait(&full[s], ph)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + s * kF8StageBytes), sf = tmem + SCALE_COL + 16u * s;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_mxfp8_pair(tmem, sdesc_sw128(sa + kk * 32u, 16u, 1024u),
+                              sdesc_sw128(sa + 16384u + kk * b_kstep, 16u, 1024u), idesc, sf, sf + 4u,
+                              kb > 0 || kk > 0 ? 1u : 0u);
+            umma_commit_pair(&empty[s], 0x3);
+          }
+          if (ok) umma_commit_pair(&accf[0], 0x3);
+        }
+        ok = false;  // the loop below is the other kind's
+      }
 #pragma unroll 1
       for (int t = pair; t < tiles && ok; t += npairs) {
 #pragma unroll 1
@@ -563,8 +616,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
     }
   } else {
     setmaxnreg_inc<kF8FoldRegs>();
-    constexpr int COLS = 4 * 256 / kF8FoldWarps;  // columns per warp
     const int q = warp & 3, part = (warp - 4) >> 2;
+    // Results leave by tiled stores of 32 rows x 128 bytes from one box per warp, so that the next tile's folding
+    // begins after a few hundred clocks (row-per-thread stores: 3.2 us a tile; what lies outside is dropped).
+    // 128 columns of the warp's 32 rows, from row mw and column n0 on; thread = row.
+    auto store128 = [&](const float2 (&acc)[64], uint8_t* box, int boxes, int mw, int n0) {
+      auto send = [&](int c, int n, const uint4 (&p)[8]) {
+        uint8_t* to = box + (boxes > 1 ? c & 1 : 0) * kF8OutBytes;
+        if (lane == 0) {
+          if (boxes > 1)
+            bulk_wait_read<1>();
+          else
+            bulk_wait_read<0>();
+        }
+        __syncwarp();
+        fp8_stage_row(to, lane, p);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (n < g.N) tma_store_2d(&tOut, to, n, mw);
+          bulk_commit();
+        }
+      };
+      if (g.out_fp32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            p[i] = make_uint4(__float_as_uint(acc[16 * c + 2 * i].x), __float_as_uint(acc[16 * c + 2 * i].y),
+                              __float_as_uint(acc[16 * c + 2 * i + 1].x), __float_as_uint(acc[16 * c + 2 * i + 1].y));
+          send(c, n0 + 32 * c, p);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint4 p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            __nv_bfloat162 h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(acc[32 * c + 4 * i + j]);
+            p[i] = *reinterpret_cast<const uint4*>(h);
+          }
+          send(c, n0 + 64 * c, p);
+        }
+      }
+    };
+    if (mx && part == 0) {
+      // Scales of each k-block into TMEM. A word holds the exponent byte of one row four times (the k-block's four MMAs
+      // share it); row 32 c + l of the 128 rows lies in lane l of column c, in all four lane quarters: this warp
+      // writes quarter q.
+      const uint32_t filled = mapa_shared(smem_u32(sff), 0);
+      const uint32_t to = tmem + SCALE_COL + ((uint32_t)(q * 32) << 16);
+      const auto word = [](float s) { return (__float_as_uint(s) >> 23 & 0xffu) * 0x01010101u; };
+      int it = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int t = pair; t < tiles && ok; t += npairs) {
+        int tm, tn;
+        fp8_tile_coords(t, m_tiles, n_tiles, tm, tn);
+        const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256;
+        const float* xs[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) xs[c] = g.xs + min(m0 + 32 * c + lane, g.T - 1);
+        const float* w0 = g.ws + (size_t)(n0 >> 7) * g.ws_n;
+        const float* w1 = n0 + 128 < g.N ? w0 + g.ws_n : w0;
+        float v[2][6];  // fetched two k-blocks ahead
+        auto fetch = [&](int kb, float (&f)[6]) {
+          if (kb >= g.nkb) return;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) f[c] = xs[c][(size_t)kb * g.T];
+          f[4] = w0[(size_t)kb * g.ws_k];
+          f[5] = w1[(size_t)kb * g.ws_k];
+        };
+        fetch(0, v[0]);
+        fetch(1, v[1]);
+#pragma unroll 1
+        for (int kb = 0; kb < g.nkb; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(&empty[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t col = to + 16u * s;
+          const uint32_t a = word(v[0][4]), b = word(v[0][5]);
+          tc_fence_after();
+          tmem_st4(col, word(v[0][0]), word(v[0][1]), word(v[0][2]), word(v[0][3]));
+          tmem_st4(col + 4, a, a, a, a);
+          tmem_st4(col + 8, b, b, b, b);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(filled + 8 * s);
+#pragma unroll
+          for (int c = 0; c < 6; ++c) v[0][c] = v[1][c];
+          fetch(kb + 2, v[1]);
+        }
+      }
+    } else if (mx) {
+      // The tile's sum: two halves of 128 columns; the accumulator goes back once the second has been read.
+      const uint32_t done = mapa_shared(smem_u32(sume), 0);
+      uint8_t* box = out_smem + (warp - 8) * 2 * kF8OutBytes;
+      int j = 0;
+#pragma unroll 1
+      for (int t = pair; t < tiles; t += npairs, ++j) {
+        int tm, tn;
+        fp8_tile_coords(t, m_tiles, n_tiles, tm, tn);
+        const int mw = tm * 256 + (int)rank * 128 + q * 32;
+        if (!mbar_wait(&accf[0], (uint32_t)j & 1u)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int n0 = tn * 256 + half * 128;
+          float2 acc[64];
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + half * 128 + c * 32 + ((uint32_t)(q * 32) << 16), v[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 64; ++c) acc[c] = make_float2(__uint_as_float(v[c / 16][2 * (c % 16)]), __uint_as_float(v[c / 16][2 * (c % 16) + 1]));
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(done);
+          }
+          if (mw < g.T && n0 < g.N) store128(acc, box, 2, mw, n0);
+        }
+      }
+    } else {
+    constexpr int COLS = 4 * 256 / kF8FoldWarps;  // columns per warp
     const uint32_t done = mapa_shared(smem_u32(acce), 0);
     int it = 0;
     bool ok = true;
@@ -578,7 +759,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
       const bool live = mw < g.T && n0 < g.N;  // of the warp
       const float* xs = g.xs + min(m, g.T - 1);
       const float* ws = g.ws + (live ? (size_t)(n0 >> 7) * g.ws_n : 0);
-      float2 acc[COLS / 2];
+      float2 acc[64];
+      static_assert(COLS == 128, "columns per folding warp");
 #pragma unroll
       for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       // Scales are fetched two k-blocks ahead and multiplied where they are used, so that nothing waits for them.
@@ -614,46 +796,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
           mbar_arrive_cluster(done + 8 * b);
         }
       }
-      // Results leave by tiled stores of 32 rows x 128 bytes from one box per warp, so that the next tile's folding
-      // begins after a few hundred clocks (row-per-thread stores: 3.2 us a tile; what lies outside is dropped).
-      if (ok && live) {
-        uint8_t* box = out_smem + (warp - 4) * kF8OutBytes;
-        auto send = [&](int c, int n, const uint4 (&p)[8]) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          fp8_stage_row(box, lane, p);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (n < g.N) tma_store_2d(&tOut, box, n, mw);
-            bulk_commit();
-          }
-        };
-        if (g.out_fp32) {
-#pragma unroll
-          for (int c = 0; c < COLS / 32; ++c) {
-            uint4 p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              p[i] = make_uint4(__float_as_uint(acc[16 * c + 2 * i].x), __float_as_uint(acc[16 * c + 2 * i].y),
-                                __float_as_uint(acc[16 * c + 2 * i + 1].x), __float_as_uint(acc[16 * c + 2 * i + 1].y));
-            send(c, n0 + 32 * c, p);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < COLS / 64; ++c) {
-            uint4 p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              __nv_bfloat162 h[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(acc[32 * c + 4 * i + j]);
-              p[i] = *reinterpret_cast<const uint4*>(h);
-            }
-            send(c, n0 + 64 * c, p);
-          }
-        }
-      }
+      if (ok && live) store128(acc, out_smem + (warp - 4) * kF8OutBytes, 1, mw, n0);
+    }
     }
     if (lane == 0) bulk_wait_all();
   }

@@ -343,6 +343,26 @@ __device__ __forceinline__ void umma_fp8_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
+// The same with every 32 K values of a row of A and of B scaled by a power of two before they are summed; the scales
+// (exponent bytes) lie in TMEM at sfa and sfb.
+__device__ __forceinline__ void umma_mxfp8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Each thread of the warp writes 4 (8) consecutive 32-bit columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Arrive once on the mbarrier at this shared offset in every CTA of cta_mask
 // when all tcgen05.mma issued so far by this thread are done.
 __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mask) {
@@ -375,6 +395,17 @@ __host__ __device__ constexpr uint32_t idesc_fp8_f32(int M, int N, bool a_e5m2, 
          | ((b_mn ? 1u : 0u) << 16)                // B major
          | ((uint32_t)(N >> 3) << 17)              // N / 8
          | ((uint32_t)(M >> 4) << 24);             // M / 16
+}
+
+// Instruction descriptor for kind::mxf8f6f4 (fp32 accumulator): the scales are powers of two, read from the lowest byte
+// of their TMEM words.
+__host__ __device__ constexpr uint32_t idesc_mxfp8(int M, int N, bool a_e5m2, bool b_e5m2, bool b_mn) {
+  return ((a_e5m2 ? 1u : 0u) << 7)                 // A format
+         | ((b_e5m2 ? 1u : 0u) << 10)              // B format
+         | ((b_mn ? 1u : 0u) << 16)                // B major
+         | ((uint32_t)(N >> 3) << 17)              // N / 8
+         | (1u << 23)                              // scale type: exponent bytes
+         | ((uint32_t)(M >> 7) << 27);             // M / 128
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle, sm_100 version field.
