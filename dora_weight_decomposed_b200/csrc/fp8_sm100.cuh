@@ -682,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
         for (int c = 0; c < 4; ++c) xs[c] = g.xs + min(m0 + 32 * c + lane, g.T - 1);
         const float* w0 = g.ws + (size_t)(n0 >> 7) * g.ws_n;
         const float* w1 = n0 + 128 < g.N ? w0 + g.ws_n : w0;
-        float v[2][6];  // fetched two k-blocks ahead
+        float v[4][6];  // fetched four k-blocks ahead, without a move that would wait for them
         auto fetch = [&](int kb, float (&f)[6]) {
           if (kb >= g.nkb) return;
 #pragma unroll
@@ -690,28 +690,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8PairThreads, 1)
           f[4] = w0[(size_t)kb * g.ws_k];
           f[5] = w1[(size_t)kb * g.ws_k];
         };
-        fetch(0, v[0]);
-        fetch(1, v[1]);
-#pragma unroll 1
-        for (int kb = 0; kb < g.nkb; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(&empty[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
-            ok = false;
-            break;
-          }
-          const uint32_t col = to + 16u * s;
-          const uint32_t a = word(v[0][4]), b = word(v[0][5]);
-          tc_fence_after();
-          tmem_st4(col, word(v[0][0]), word(v[0][1]), word(v[0][2]), word(v[0][3]));
-          tmem_st4(col + 4, a, a, a, a);
-          tmem_st4(col + 8, b, b, b, b);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(filled + 8 * s);
 #pragma unroll
-          for (int c = 0; c < 6; ++c) v[0][c] = v[1][c];
-          fetch(kb + 2, v[1]);
+        for (int u = 0; u < 4; ++u) fetch(u, v[u]);
+#pragma unroll 1
+        for (int kb4 = 0; kb4 < g.nkb && ok; kb4 += 4) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int kb = kb4 + u;
+            if (kb >= g.nkb) break;
+            const int s = it % STAGES;
+            if (!mbar_wait(&empty[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
+              ok = false;
+              break;
+            }
+            const uint32_t col = to + 16u * s;
+            const uint32_t a = word(v[u][4]), b = word(v[u][5]);
+            tc_fence_after();
+            tmem_st4(col, word(v[u][0]), word(v[u][1]), word(v[u][2]), word(v[u][3]));
+            tmem_st4(col + 4, a, a, a, a);
+            tmem_st4(col + 8, b, b, b, b);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(filled + 8 * s);
+            fetch(kb + 4, v[u]);
+            ++it;
+          }
         }
       }
     } else if (mx) {

@@ -92,29 +92,43 @@ def dora_fp8_quantize(x, *, block: str = "row", dtype=None, q=None, scale=None, 
     [ceil(rows / 128), ceil(cols / 128)] by tile; dtype is float8_e4m3fn
     (default) or float8_e5m2; cols is a multiple of 16.
     """
+    sig = (block, x.shape, x.dtype, dtype)
+    plan = _QUANTIZE_PLANS.get(sig) or _quantize_plan(sig, x)
+    code, out, how, shape, qtype, call = plan
+    dev = x.device
+    _current(dev)
+    f32 = _torch().float32
+    if q is None:
+        q = x.new_empty(x.shape, dtype=qtype) if stream is None else _empty(x.shape, qtype, dev, stream)
+    else:
+        _tensor(q, x.shape, qtype, dev, "q")
+    if scale is None:
+        scale = x.new_empty(shape, dtype=f32) if stream is None else _empty(shape, f32, dev, stream)
+    else:
+        _tensor(scale, shape, f32, dev, "scale")
+    _check(call(x.shape[0], x.shape[1], code, out, how, _ptr(x), _ptr(q), _ptr(scale), _stream(stream, dev)))
+    return q, scale
+
+
+_QUANTIZE_PLANS: dict = {}
+
+
+def _quantize_plan(sig, x):
+    """Check one signature; (code of x, code of q, block, shape of the scales, type of q, library call)."""
     torch = _torch()
-    lib = load_library()
+    block, _, xtype, dtype = sig
     if block not in _BLOCKS:
         raise ValueError(f"block is {block!r}, expected 'row' or 'tile'")
     if x.dim() != 2:
         raise ValueError(f"x has {x.dim()} dimensions, expected 2")
     dtype = torch.float8_e4m3fn if dtype is None else dtype
-    code, out = _code(x.dtype, "x", _WIDE), _code(dtype, "dtype", _EIGHT)
+    code, out = _code(xtype, "x", _WIDE), _code(dtype, "dtype", _EIGHT)
     rows, cols = x.shape
-    dev = x.device
     shape = (-(-cols // 128), rows) if block == "row" else (-(-rows // 128), -(-cols // 128))
-    _current(dev)
-    if q is None:
-        q = _empty((rows, cols), dtype, dev, stream)
-    else:
-        _tensor(q, (rows, cols), dtype, dev, "q")
-    if scale is None:
-        scale = _empty(shape, torch.float32, dev, stream)
-    else:
-        _tensor(scale, shape, torch.float32, dev, "scale")
-    _check(lib.dora_fp8_quantize(rows, cols, code, out, _BLOCKS[block], _ptr(x), _ptr(q), _ptr(scale),
-                                 _stream(stream, dev)))
-    return q, scale
+    if len(_QUANTIZE_PLANS) > 4096:
+        _QUANTIZE_PLANS.clear()
+    plan = _QUANTIZE_PLANS[sig] = (code, out, _BLOCKS[block], shape, dtype, load_library().dora_fp8_quantize)
+    return plan
 
 
 @functools.lru_cache(maxsize=4096)
