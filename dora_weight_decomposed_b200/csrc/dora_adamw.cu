@@ -113,7 +113,6 @@ __device__ __forceinline__ float2 add_rounded(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
 // ------------------------------------------------------------------ loads and stores of 8 elements
 
@@ -343,14 +342,12 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 // 0 <= y <= 448 as an e4m3 code, floor(y / step + u / 65536) with step the code spacing at y, in the top byte of the
-// result (below its top bit). From 2^-6 up the spacing is 2^-3 of the binade, so the code is the top bits of the fp32
+// result (its top bit clear). From 2^-6 up the spacing is 2^-3 of the binade, so the code is the top bits of the fp32
 // pattern (exponent offset 120) after u is added below them. Under 2^-6 it is 2^-9 throughout, and adding 2^-6 brings
 // the same bits into the same place (offset 121). Doubling y moves the first offset to 121 too, and the larger of
-// the two is the one that holds. least: 2^-6 (1 + k / 8) makes it code k at least. u16 = 16 u.
-// twice = 2 y, low = y + 2^-6.
-__device__ __forceinline__ uint32_t stochastic_code(float twice, float low, uint32_t u16, float least) {
-  const float t = fmaxf(fmaxf(twice, low), least);
-  return (__float_as_uint(t) + u16 - (121u << 23)) << 4;
+// the two (t) is the one that holds. u: 16 bits.
+__device__ __forceinline__ uint32_t stochastic_code(float t, uint32_t u) {
+  return (__float_as_uint(t) + (u << 4)) * 16u - (121u << 27);
 }
 
 // The scale of a block of 16 lanes x 8 moments (all of the warp's lanes take part); not finite if one of them is not.
@@ -371,10 +368,10 @@ __device__ __forceinline__ float moment_scale(const float2 (&v)[4]) {
   return s;
 }
 
-// a / b rounded to nearest from the rounded reciprocal of b (Markstein's quotient step).
-__device__ __forceinline__ float2 quotient(float2 a, float b, float inv_b) {
+// a / b rounded to nearest from the rounded reciprocal of b (Markstein's quotient step); minus_b = -b.
+__device__ __forceinline__ float2 quotient(float2 a, float minus_b, float inv_b) {
   const float2 q = mul2(a, both(inv_b));
-  return fma2(fma2(neg2(q), both(b), a), both(inv_b), q);
+  return fma2(fma2(q, both(minus_b), a), both(inv_b), q);
 }
 
 // sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2 (to the last place); zero for v = 0, NaN for inf.
@@ -383,7 +380,7 @@ __device__ __forceinline__ float2 root(float2 v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1e-37f)));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1e-37f)));
   const float2 s = mul2(v, y);
-  return fma2(fma2(neg2(s), s, v), mul2(y, both(0.5f)), s);
+  return fma2(fma2(mul2(s, both(-1.0f)), s, v), mul2(y, both(0.5f)), s);
 }
 
 __device__ __forceinline__ float reciprocal(float v) {
@@ -493,18 +490,29 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     const float im = inverse(sm), ir = inverse(sr);
     uint32_t zm[8], zr[8];
     const uint32_t pair0 = e.index0 + (uint32_t)(i >> 1);
+    // sqrt(v) > 0 is held as code 1 at least: t = 2^-6 (1 + 1 / 8).
+    constexpr float kOne = 0.017578125f;
+    float least = fminf(fminf(r[0].x, r[0].y), fminf(r[1].x, r[1].y));
+    least = fminf(least, fminf(fminf(r[2].x, r[2].y), fminf(r[3].x, r[3].y)));
+    const bool some_zero = !(least > 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t h = mix((pair0 + j) ^ c.key);
-      const uint32_t u0 = h << 4 & 0xffff0u, u1 = h >> 12 & 0xffff0u;
-      const float2 ym = quotient(m[j], sm, im), yr = quotient(r[j], sr, ir);
+      const uint32_t u0 = h & 0xffffu, u1 = h >> 16;
+      const float2 ym = quotient(m[j], -sm, im), yr = quotient(r[j], -sr, ir);
       const float2 am = make_float2(fabsf(ym.x), fabsf(ym.y));
       const float2 tm = add2(am, am), lm = add2(am, both(0.015625f)), tr = add2(yr, yr), lr = add2(yr, both(0.015625f));
-      zm[2 * j] = stochastic_code(tm.x, lm.x, u0, 0.f) | (__float_as_uint(ym.x) & 0x80000000u);
-      zm[2 * j + 1] = stochastic_code(tm.y, lm.y, u1, 0.f) | (__float_as_uint(ym.y) & 0x80000000u);
-      // sqrt(v) > 0 is held as code 1 at least
-      zr[2 * j] = stochastic_code(tr.x, lr.x, u0, r[j].x > 0.f ? 0.017578125f : 0.f);
-      zr[2 * j + 1] = stochastic_code(tr.y, lr.y, u1, r[j].y > 0.f ? 0.017578125f : 0.f);
+      zm[2 * j] = stochastic_code(fmaxf(tm.x, lm.x), u0) | (__float_as_uint(ym.x) & 0x80000000u);
+      zm[2 * j + 1] = stochastic_code(fmaxf(tm.y, lm.y), u1) | (__float_as_uint(ym.y) & 0x80000000u);
+      zr[2 * j] = stochastic_code(fmaxf(fmaxf(tr.x, lr.x), kOne), u0);
+      zr[2 * j + 1] = stochastic_code(fmaxf(fmaxf(tr.y, lr.y), kOne), u1);
+    }
+    if (some_zero) {  // a zero moment (padding, a row without gradient) stays zero
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!(r[j].x > 0.f)) zr[2 * j] = 0;
+        if (!(r[j].y > 0.f)) zr[2 * j + 1] = 0;
+      }
     }
     cm = make_uint2(top_bytes(zm[0], zm[1], zm[2], zm[3]), top_bytes(zm[4], zm[5], zm[6], zm[7]));
     cr = make_uint2(top_bytes(zr[0], zr[1], zr[2], zr[3]), top_bytes(zr[4], zr[5], zr[6], zr[7]));

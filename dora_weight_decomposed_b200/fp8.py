@@ -59,20 +59,31 @@ def _tensor(t, shape, dtype, device, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+_current_device = None  # torch.cuda.current_device, set on first use
+
+
 def _current(device) -> None:
+    global _current_device
     if device.type == "cuda":
-        torch = _torch()
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}; "
+        if _current_device is None:
+            _current_device = _torch().cuda.current_device
+        if device.index != _current_device():
+            raise ValueError(f"tensors are on {device}, but the current device is cuda:{_current_device()}; "
                              f"call under torch.cuda.device({device.index})")
+
+
+_raw_stream = None  # device index -> handle of its current stream, set on first use
 
 
 def _stream(stream, device):
     """_stream_ptr, without building a stream object for the current stream (a third of a small call's host time)."""
+    global _raw_stream
     if stream is None and device.type == "cuda":
-        raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(device.index) or None
+        if _raw_stream is None:
+            torch = _torch()
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
+        return _raw_stream(device.index) or None
     return _stream_ptr(stream)
 
 
@@ -190,8 +201,14 @@ def _product(op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype, ws, st
         nbytes = ws.numel() * ws.element_size()
     elif need:
         ws = _empty(need, _torch().uint8, dev, stream)
-    _check(call(ref, shape[0], _ptr(x), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
-                _stream(stream, dev)))
+    if x.is_cuda and x.is_contiguous() and wq.is_contiguous() and w_scale.is_contiguous():  # all on one device, by the plan
+        status = call(ref, shape[0], x.data_ptr(), _ptr(x_scale), wq.data_ptr(), w_scale.data_ptr(), _ptr(out), _ptr(ws),
+                      nbytes, _stream(stream, dev))
+    else:  # the message of the one that is refused
+        status = call(ref, shape[0], _ptr(x), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
+                      _stream(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
