@@ -6,7 +6,12 @@ the oracle's. Products: with a_tk = |x_scale xq|, b_nk = |w_scale wq| the sum of
 128 * 2^-23 of the block's sum of |products| (one unit in the last place per
 addition, rounded or cut off), and folding nkb blocks with a rounded scale by at most
 (nkb + 3) * 2^-24 of the whole; the result is then rounded once, by at most
-half a step of the output type.
+half a step of the output type. Above 128 tokens, when every scale is a power of
+two, the tensor core applies the scales (exactly) and adds all K products of a
+result in the one accumulator: then the first bound is K * 2^-23 of the sum of
+|products|. If those K roundings are independent, their sum is off by about
+sqrt(K) * 2^-24 of the largest partial sum, so the whole matrix is also held to
+sqrt(K) * 2^-22 of its norm (and the output's rounding).
 """
 import numpy as np
 import pytest
@@ -104,10 +109,14 @@ def weight(d_out, d_in, seed=1, pow2=False):
     return w, torch.from_numpy(s.astype(np.float32)).cuda()
 
 
-def check_product(out, a, b, K, what=""):
-    """out against a @ b (float64), by the bound of the module's first lines."""
+def check_product(out, a, b, K, what="", powers=False):
+    """out against a @ b (float64), by the bounds of the module's first lines; powers: every scale is a power of two."""
     ref, mag = a @ b, np.abs(a) @ np.abs(b)
-    tol = (128 * 2.0 ** -23 + (-(-K // 128) + 3) * 2.0 ** -24) * mag
+    sums = K if powers and len(a) > 128 else 128
+    tol = (sums * 2.0 ** -23 + (-(-K // 128) + 3) * 2.0 ** -24) * mag
+    if not np.isnan(ref).any():
+        far = np.linalg.norm(host(out) - ref) / max(np.linalg.norm(ref), 1e-300)
+        assert far <= np.sqrt(K) * 2.0 ** -22 + HALF[out.dtype], (what, far)
     tol = tol + HALF[out.dtype] * (np.abs(ref) + tol)
     # An 8-bit NaN among the operands (the conversion of values beyond the type's range gives one) is a NaN in the result.
     nan = np.isnan(ref)
@@ -155,17 +164,43 @@ def test_products_of_wide_operands(T, d_out, d_in, dtype, backward):
         out = fn(x, wq, ws, fp8_dtype=fp8)
         assert out.dtype == dtype
         q, s = of.quantize(host(x), NAME[fp8], False)
-        check_product(out, of.widen_rows(q, s), w if backward else w.T, K, fp8)
+        check_product(out, of.widen_rows(q, s), w if backward else w.T, K, fp8, powers=True)
         # the two-call form gives the same bits
         xq, xs = dw.dora_fp8_quantize(x, dtype=fp8)
         two = fn(xq, wq, ws, out_dtype=dtype, **{"dy_scale" if backward else "x_scale": xs})
         assert torch.equal(out, two)
 
 
-@pytest.mark.parametrize("T", [1, 9, 140])
-def test_non_finite_rows_stay_in_their_rows(T):
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("T,d_out,d_in", [(129, 256, 128), (256, 272, 1168), (300, 528, 400), (517, 1040, 272), (140, 144, 27648)])
+def test_scales_that_are_powers_of_two_and_others(T, d_out, d_in, backward):
+    """The tensor cores apply the scales of the first call; one scale of the weight, or of the operand, in the later ones
+    is no power of two, zero, negative or subnormal, and those are applied in fp32."""
+    K = d_out if backward else d_in
+    fn = dw.dora_fp8_backward if backward else dw.dora_fp8_forward
+    rng = np.random.default_rng(T)
+    xq = torch.from_numpy(rng.standard_normal((T, K)) * 50).cuda().to(E4)
+    wq = torch.from_numpy(rng.standard_normal((d_out, d_in)) * 50).cuda().to(E4)
+    xs0 = torch.from_numpy(np.exp2(rng.integers(-20, 20, (-(-K // 128), T))).astype(np.float32)).cuda()
+    ws0 = torch.from_numpy(np.exp2(rng.integers(-9, 9, (-(-d_out // 128), -(-d_in // 128)))).astype(np.float32)).cuda()
+    key = "dy_scale" if backward else "x_scale"
+    for what, at, v in (("powers", None, 1), ("weight", "w", 1.5), ("operand", "x", 0.7), ("zero", "w", 0.0), ("negative", "w", -2.0),
+                        ("subnormal", "x", 1e-40)):
+        xs, ws = xs0.clone(), ws0.clone()
+        if at == "w":
+            ws.view(-1)[-1] = v
+        elif at == "x":
+            xs.view(-1)[xs.numel() // 2] = v
+        out = fn(xq, wq, ws, out_dtype=torch.float32, **{key: xs})
+        w = of.widen_tiles(host(wq), host(ws))
+        check_product(out, of.widen_rows(host(xq), host(xs)), w if backward else w.T, K, what, powers=what == "powers")
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("T", [1, 9, 140, 300])
+def test_non_finite_rows_stay_in_their_rows(T, pow2):
     x = matrix(T, 384, torch.bfloat16, wide=False)
-    wq, ws = weight(272, 384)
+    wq, ws = weight(272, 384, pow2=pow2)
     clean = dw.dora_fp8_forward(x, wq, ws)
     x[0, 200] = float("inf")
     if T > 5:
@@ -207,7 +242,8 @@ def test_gradient_by_differences(T):
     w = of.widen_tiles(host(wq), host(ws))
     # three results, each an fp32 sum within the products' bound of its sum of magnitudes (|x| <= 15 here)
     mag = float((np.abs(host(dy)) @ np.abs(w)).sum()) * 15 * 2 + float((np.abs(host(dy)) @ np.abs(w) * np.abs(host(dirn))).sum())
-    assert abs(diff - want) <= (128 * 2.0 ** -23 + 10 * 2.0 ** -24) * mag
+    sums = 400 if T > 128 else 128  # products added in one accumulator (d_in = 400, d_out = 272)
+    assert abs(diff - want) <= (sums * 2.0 ** -23 + 10 * 2.0 ** -24) * mag
 
 
 def test_stream_and_graph():
