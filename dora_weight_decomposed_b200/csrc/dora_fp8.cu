@@ -17,38 +17,41 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // ------------------------------------------------------------------ quantisation
 
 // 1 x 128 blocks. It lets the next grid start only once all work before it is done, so that a product which
-// follows it may read the weight at once. A warp takes 16 rows of one column block, 16 lanes of 8 values per block and all eight of its loads
+// follows it may read the weight at once. A warp takes 2 R rows of one column block, 16 lanes of 8 values per block and all R of its loads
 // in flight; the CTA's eight warps take neighbouring column blocks. Bound by HBM.
-// ws, flag: in front of a product, the first CTA also says whether all n_ws scales of the weight are powers of two.
-template <class T, bool E5M2>
+// ws, flag: in front of a product, one more CTA (the last in x) says whether all n_ws scales of the weight are powers
+// of two. R: loads per thread; 2 R rows per warp.
+template <class T, bool E5M2, int R>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                 uint8_t* __restrict__ q, float* __restrict__ scale,
                                                                 const float* __restrict__ ws, int n_ws, int* flag) {
   pdl_wait();
   pdl_trigger();
-  if (flag && blockIdx.x == 0 && blockIdx.y == 0) {
+  if (flag && blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y > 0) return;
     bool all = true;
 #pragma unroll 4
     for (int i = threadIdx.x; i < n_ws; i += 256) all = all && is_power(ws[i]);
     all = __syncthreads_and(all);
     if (threadIdx.x == 0) *flag = all ? 1 : 0;
+    return;
   }
   const int kb = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (kb >= nkb) return;
   const int sub = threadIdx.x & 15, h = (threadIdx.x >> 4) & 1;
-  const int c = kb * 128 + sub * 8, r0 = blockIdx.x * 16 + h;
+  const int c = kb * 128 + sub * 8, r0 = blockIdx.x * (2 * R) + h;
   const size_t at = (size_t)r0 * cols + c;
-  Raw8<T> raw[8];
+  Raw8<T> raw[R];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < R; ++i) {
     if (c < cols && r0 + 2 * i < rows)
       raw[i].load(x + at + (size_t)(2 * i) * cols);
     else
       raw[i].clear();
   }
-  float mine = 0.f;  // lane `sub` keeps the scale of its half's row `sub`, so that 16 rows' scales are stored together
+  float mine = 0.f;  // lane `sub` keeps the scale of its half's row `sub`, so that 2 R rows' scales are stored together
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < R; ++i) {
     float amax = raw[i].absmax();
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = absmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restr
     if (c < cols && r0 + 2 * i < rows)
       *reinterpret_cast<uint2*>(q + at + (size_t)(2 * i) * cols) = to_fp8x8<E5M2>(v, s.inv);
   }
-  if (sub < 8 && r0 + 2 * sub < rows) scale[(size_t)kb * rows + r0 + 2 * sub] = mine;
+  if (sub < R && r0 + 2 * sub < rows) scale[(size_t)kb * rows + r0 + 2 * sub] = mine;
 }
 
 // 128 x 128 blocks: one CTA each, 16 lanes per row, 8 rows per thread held in registers between the maximum and the
@@ -132,8 +135,13 @@ cudaError_t quantize_t(int64_t rows, int64_t cols, bool tiles, const void* x, vo
   if (tiles)
     return launch_pdl(fp8_quantize_tiles_kernel<T, E5M2>, dim3((unsigned)(cdiv(rows, 128) * nkb)), dim3(256), 0, st,
                       (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale);
-  return launch_pdl(fp8_quantize_rows_kernel<T, E5M2>, dim3((unsigned)cdiv(rows, 16), (unsigned)cdiv(nkb, 8)), dim3(256),
-                    0, st, (const T*)x, (int)rows, (int)cols, nkb, (uint8_t*)q, scale, wc.ws, wc.n, wc.flag);
+  // Eight loads per thread while that makes a CTA for every SM (4096 x 8192: 18.7 us, 31 us with one load), else one:
+  // small operands are bound by the length of a thread's work.
+  const bool few = cdiv(rows, 16) * cdiv(nkb, 8) < device_sm_count();
+  const int64_t groups = cdiv(rows, few ? 2 : 16) + (wc.flag ? 1 : 0);
+  return launch_pdl(few ? fp8_quantize_rows_kernel<T, E5M2, 1> : fp8_quantize_rows_kernel<T, E5M2, 8>,
+                    dim3((unsigned)groups, (unsigned)cdiv(nkb, 8)), dim3(256), 0, st, (const T*)x, (int)rows, (int)cols, nkb,
+                    (uint8_t*)q, scale, wc.ws, wc.n, wc.flag);
 }
 
 cudaError_t quantize(int64_t rows, int64_t cols, dora_dtype_t in, dora_dtype_t fp8, bool tiles, const void* x, void* q,
