@@ -316,6 +316,7 @@ bool check_fp8_desc(const dora_fp8_desc_t* d) {
   if (!d) return set_error("desc is NULL"), false;
   if (d->d_out < 1 || d->d_in < 1) return set_error("d_out and d_in must be >= 1"), false;
   if (d->d_out > kMaxDim || d->d_in > kMaxDim) return set_error("d_out or d_in too large"), false;
+  if (cdiv(d->d_out, 128) * cdiv(d->d_in, 128) > INT32_MAX) return set_error("weight too large"), false;
   if (d->d_out % 16 || d->d_in % 16) return set_error("8-bit layers need d_out and d_in to be multiples of 16"), false;
   if (!is_fp8(d->in_dtype) && !is_wide(d->in_dtype)) return set_error("desc->in_dtype is not a dora_dtype_t"), false;
   if (!is_fp8(d->in_dtype) && !is_fp8(d->fp8_dtype))

@@ -143,8 +143,9 @@ def _quantize_plan(sig, x):
 
 
 @functools.lru_cache(maxsize=4096)
-def _desc_and_workspace(d_out: int, d_in: int, in_code: int, fp8_code: int, out_code: int, T: int, op: int):
-    """The C descriptor of these sizes and types (a byref of it) and the workspace they need."""
+def _desc_and_workspace(d_out: int, d_in: int, in_code: int, fp8_code: int, out_code: int, T: int, op: int, device):
+    """The C descriptor of these sizes and types (a byref of it) and the workspace they need on the current device
+    (`device` is its index)."""
     desc = Fp8Desc(d_out, d_in, in_code, fp8_code, out_code)
     ref = ctypes.byref(desc)
     return ref, int(load_library().dora_fp8_workspace_size(ref, T, op))
@@ -175,7 +176,8 @@ def _plan(sig, op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype):
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16 if given else dtype
     fcode = DORA_E4M3 if fp8_dtype is None else _code(fp8_dtype, "fp8_dtype", _EIGHT)
-    ref, need = _desc_and_workspace(d_out, d_in, code, fcode, _code(out_dtype, "out_dtype", _WIDE), T, op)
+    _current(dev)
+    ref, need = _desc_and_workspace(d_out, d_in, code, fcode, _code(out_dtype, "out_dtype", _WIDE), T, op, dev.index)
     plan = (ref, need, given, (T, N), out_dtype, lib.dora_fp8_forward if op == DORA_FP8_OP_FORWARD else lib.dora_fp8_backward)
     if len(_PLANS) > 4096:
         _PLANS.clear()
@@ -219,7 +221,8 @@ def dora_fp8_workspace_size(d_out: int, d_in: int, in_dtype, T: int, op: int, *,
     code = _code(in_dtype, "in_dtype", _BOTH)
     out = torch.bfloat16 if out_dtype is None and code > 1 else (in_dtype if out_dtype is None else out_dtype)
     return _desc_and_workspace(int(d_out), int(d_in), code, _code(fp8_dtype or torch.float8_e4m3fn, "fp8_dtype", _EIGHT),
-                               _code(out, "out_dtype", _WIDE), int(T), int(op))[1]
+                               _code(out, "out_dtype", _WIDE), int(T), int(op),
+                               torch.cuda.current_device() if torch.cuda.is_available() else None)[1]
 
 
 def dora_fp8_forward(x, wq, w_scale, *, x_scale=None, out_dtype=None, fp8_dtype=None, y=None, ws=None, stream=None):
