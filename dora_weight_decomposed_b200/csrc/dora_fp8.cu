@@ -22,7 +22,7 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // ws, flag: in front of a product, one more CTA (the last in x) says whether all n_ws scales of the weight are powers
 // of two. R: loads per thread; 2 R rows per warp.
 template <class T, bool E5M2, int R>
-__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) fp8_quantize_rows_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                 uint8_t* __restrict__ q, float* __restrict__ scale,
                                                                 const float* __restrict__ ws, int n_ws, int* flag) {
   pdl_wait();
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T* __restr
 // 128 x 128 blocks: one CTA each, 16 lanes per row, 8 rows per thread held in registers between the maximum and the
 // codes, so that the matrix is read once. Bound by HBM.
 template <class T, bool E5M2>
-__global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) fp8_quantize_tiles_kernel(const T* __restrict__ x, int rows, int cols, int nkb,
                                                                  uint8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ float red[8];
   pdl_trigger();
