@@ -284,7 +284,7 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
 
 // What a call keeps in its workspace (the quantised operand and its scales), unless the kernel quantises it itself.
 struct Fp8Plan {
-  bool own_x = false, narrow = true;
+  bool own_x = false, narrow = true, flags = false;
   size_t off_q = 0, off_s = 0, off_flags = 0, total = 0;
 };
 
@@ -297,7 +297,8 @@ Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
   const int64_t K = back ? d.d_out : d.d_in, N = back ? d.d_in : d.d_out, nkb = cdiv(K, 128);
   if (T == 0) return p;
   p.narrow = T <= 128;
-  if (!p.narrow) p.total = kF8MaxFlags * sizeof(int);  // the pair kernel's flags
+  p.flags = !p.narrow && (d.out_dtype == DORA_BF16 || nkb <= kF8MaxBlocksFp32);
+  if (p.flags) p.total = kF8MaxFlags * sizeof(int);
   if (is_fp8(d.in_dtype)) return p;
   if (T <= 16 && nkb <= 8 * Fp8Narrow<16>::STAGES) {
     const int64_t tiles = cdiv(N, 128);
@@ -348,7 +349,7 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   const void* xq = x;
   const int n_ws = (int)(cdiv(desc->d_out, 128) * cdiv(desc->d_in, 128));
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-  int* flags = p.narrow ? nullptr : reinterpret_cast<int*>(w + p.off_flags);
+  int* flags = p.flags ? reinterpret_cast<int*>(w + p.off_flags) : nullptr;
   int n_flags = 1;
   if (!given && !p.own_x) {
     const cudaError_t e = quantize(T, K, desc->in_dtype, type, false, x, w + p.off_q, reinterpret_cast<float*>(w + p.off_s),
