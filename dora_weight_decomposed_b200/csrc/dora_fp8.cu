@@ -175,7 +175,7 @@ cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t
 
 // Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
 // answer of the occupancy query, which counts one CTA per SM for the narrow kernels; asked once per device.
-template <int NT, bool W_MN, class XT>
+template <int NT, bool W_MN>
 int clusters_alone(int cs) {
   static std::atomic<int> known[64][9];
   int dev = 0;
@@ -192,7 +192,7 @@ int clusters_alone(int cs) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, XT>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, void>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = std::max(1, device_sm_count() / cs * 7 / 8);
     }
@@ -202,29 +202,54 @@ int clusters_alone(int cs) {
   return n;
 }
 
-// The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two, and 256
-// CTAs of one launch were seen to start together): twice as many, or one on every (cs + 1) / 2 SMs.
-template <int NT, bool W_MN, class XT>
+// The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two): twice as
+// many. Seen in the times: 48 tiles in one wave with 5 splits and in two with 6, 96 tiles with 2 and 3. The small CTAs of
+// 16 tokens also fit as one cluster on every (cs + 1) / 2 SMs: 32 tiles with 8 splits in one wave, which at 128 tokens
+// (256 x 2048 x 2048) took 12.2 us, and 9.5 with 6.
+template <int NT, bool W_MN>
 int narrow_slots(int cs) {
-  return std::max(2 * clusters_alone<NT, W_MN, XT>(cs), clusters_alone<NT, W_MN, XT>((cs + 1) / 2));
+  const int twice = 2 * clusters_alone<NT, W_MN>(cs);
+  return NT == 16 ? std::max(twice, clusters_alone<NT, W_MN>((cs + 1) / 2)) : twice;
 }
 
-// CTAs per tile of the narrow kernel (K splits, one cluster): the count with the least estimated time, in k-blocks:
-// waves of clusters times the k-blocks of a split plus what a CTA costs beside them, 2 to start and fill and 2 more
-// to add the splits. T = 37 of 27648 x 5120 takes 31.3 us with its 216 tiles in one wave, 36.5 us with two splits
-// and 432 CTAs in two waves; T = 16 of 8192 x 8192 17.7 us with 4 splits (256 CTAs), 22.3 us with 8 (two waves).
-template <int NT, bool W_MN, class XT>
-int narrow_splits(int64_t tiles, int64_t nkb) {
-  int best = 1;
-  double best_t = 1e300;
-  for (int cs = 1; cs <= 8 && cs <= nkb; ++cs) {
-    const double t = (double)cdiv(tiles, narrow_slots<NT, W_MN, XT>(cs)) * ((double)cdiv(nkb, cs) + (cs > 1 ? 4.0 : 2.0));
-    if (t < best_t - 1e-9) {
-      best_t = t;
-      best = cs;
+// CTAs per tile of the narrow kernel (K splits, one cluster) and the call's estimated time in microseconds: waves of
+// clusters, in each 0.43 us per k-block where a CTA has its SM and 0.6 where two share it, which is what the operands'
+// way in allows, 1 us to fill and, with splits, 2 us and 2 more at 128 tokens to add them; and 4 for the launch and the
+// store. Measured around the chosen count: T = 1 of 4096 x 4096 7.2 us with 8 splits, 7.8 with 7; T = 37 of
+// 27648 x 5120 27.8 with 1, 33.6 with 2; its backward call, 40 tiles of 216 k-blocks, 28.9 with 5, 28.7 with 6 and 42
+// with 7 (two waves); T = 100 of 8192 x 8192 21.4 with 3, 20.6 with 4 and 28.9 with 5.
+struct NarrowChoice {
+  int cs = 1;
+  double us = 1e300;
+};
+template <int NT, bool W_MN>
+NarrowChoice narrow_choice(int64_t tiles, int64_t nkb, int64_t least = 1) {
+  NarrowChoice best;
+  const int sms = device_sm_count();
+  for (int cs = (int)least; cs <= 8 && cs <= nkb; ++cs) {
+    const double block = tiles * cs > sms ? 0.6 : 0.43, add = cs > 1 ? 2.0 + NT / 64.0 : 0.0;
+    const int64_t waves = cdiv(tiles, narrow_slots<NT, W_MN>(cs));
+    const double us = (double)waves * ((double)cdiv(nkb, cs) * block + add + 1.0) + 4.0;
+    if (us < best.us - 1e-9) {
+      best.us = us;
+      best.cs = cs;
     }
   }
   return best;
+}
+
+// The least number of splits that leaves a CTA no more k-blocks than the ring's stages, so that the kernel can quantise x
+// itself, or 0 where the device's 2 CTAs per SM do not allow as many. Not by what clusters fit: those differ from one
+// device to the next, and a workspace asked for on one of them has to do on another.
+int64_t few_blocks_splits(int64_t T, int64_t N, int64_t nkb) {
+  const int64_t most = std::clamp<int64_t>(2 * device_sm_count() / cdiv(N, 128), 1, 8), least = cdiv(nkb, Fp8Narrow<16>::STAGES);
+  return T <= 16 && least <= most ? least : 0;
+}
+
+// The pair kernel's time: waves of 256 x 256 tiles, 0.44 us per k-block, up to 0.56 with every pair busy, plus 6.
+double pair_us(int64_t T, int64_t N, int64_t nkb) {
+  const int64_t pairs = std::max(1, device_sm_count() / 2), tiles = cdiv(T, 256) * cdiv(N, 256);
+  return (double)cdiv(tiles, pairs) * (double)nkb * (0.44 + 0.12 * (double)std::min(tiles, pairs) / (double)pairs) + 6.0;
 }
 
 template <int NT, bool W_MN, class XT>
@@ -234,7 +259,8 @@ cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp
   cudaError_t e = set_smem_once(smem_set, kern, Fp8Narrow<NT>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
-  const int cs = narrow_splits<NT, W_MN, XT>(tiles * t_tiles, g.nkb);
+  // (The same splits for an x that comes in codes as for one that is quantised here: the same sums.)
+  const int cs = narrow_choice<NT, W_MN>(tiles * t_tiles, g.nkb, std::max<int64_t>(1, few_blocks_splits(g.T, g.N, g.nkb))).cs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * t_tiles * cs));
   cfg.blockDim = dim3(kF8Threads);
@@ -258,7 +284,8 @@ cudaError_t launch_narrow_nt(int nt, const CUtensorMap& tw, const CUtensorMap& t
   switch (nt) {
     case 16: return launch_narrow<16, W_MN, void>(tw, tx, g, early_w, st);
     case 32: return launch_narrow<32, W_MN, void>(tw, tx, g, early_w, st);
-    default: return launch_narrow<64, W_MN, void>(tw, tx, g, early_w, st);
+    case 64: return launch_narrow<64, W_MN, void>(tw, tx, g, early_w, st);
+    default: return launch_narrow<128, W_MN, void>(tw, tx, g, early_w, st);
   }
 }
 
@@ -293,19 +320,21 @@ bool is_wide(dora_dtype_t t) { return t == DORA_BF16 || t == DORA_FP32; }
 
 Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
   Fp8Plan p;
-  const bool back = op == DORA_FP8_OP_BACKWARD, bf16 = d.in_dtype == DORA_BF16;
+  const bool back = op == DORA_FP8_OP_BACKWARD;
   const int64_t K = back ? d.d_out : d.d_in, N = back ? d.d_in : d.d_out, nkb = cdiv(K, 128);
   if (T == 0) return p;
-  p.narrow = T <= 128;
-  p.flags = !p.narrow && (d.out_dtype == DORA_BF16 || nkb <= kF8MaxBlocksFp32);
-  if (p.flags) p.total = kF8MaxFlags * sizeof(int);
-  if (is_fp8(d.in_dtype)) return p;
-  if (T <= 16 && nkb <= 8 * Fp8Narrow<16>::STAGES) {
-    const int64_t tiles = cdiv(N, 128);
-    const int cs = back ? (bf16 ? narrow_splits<16, true, __nv_bfloat16>(tiles, nkb) : narrow_splits<16, true, float>(tiles, nkb))
-                        : (bf16 ? narrow_splits<16, false, __nv_bfloat16>(tiles, nkb) : narrow_splits<16, false, float>(tiles, nkb));
-    p.own_x = cdiv(nkb, cs) <= Fp8Narrow<16>::STAGES;
+  // Tiles of up to 128 tokens with K split over clusters, or 256 x 256 tiles on CTA pairs: the latter need many
+  // tiles (T = 512: 1024 x 8192 20 us narrow and 34 us on pairs, 4096 x 4096 18.4 and 21.1, 8192 x 8192 43.3 and 42.1,
+  // 6144 x 2048 15.9 and 15.0).
+  if (T > 128) {
+    const int64_t tiles = cdiv(N, 128) * cdiv(T, 128);
+    const double us = back ? narrow_choice<128, true>(tiles, nkb).us : narrow_choice<128, false>(tiles, nkb).us;
+    p.narrow = us < pair_us(T, N, nkb);
   }
+  p.flags = !p.narrow && (d.out_dtype == DORA_BF16 || nkb <= kF8MaxBlocksFp32);
+  if (T > 128) p.total = kF8MaxFlags * sizeof(int);  // the choice may differ between devices, the workspace may not
+  if (is_fp8(d.in_dtype)) return p;
+  p.own_x = few_blocks_splits(T, N, nkb) > 0;
   if (p.own_x) return p;
   p.off_q = p.total;
   p.off_s = p.off_q + align256((size_t)T * K);
@@ -367,7 +396,7 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
   }
   const int nkw = (int)cdiv(desc->d_in, 128);  // columns of w_scale
   Fp8Geom g{x, (int)K, x_scale, w_scale, out, (int)T, (int)N, (int)cdiv(K, 128), backward ? 1 : nkw, backward ? nkw : 1,
-            desc->out_dtype == DORA_FP32, type == DORA_E5M2, flags, flags ? n_flags : 0};
+            desc->out_dtype == DORA_FP32, type == DORA_E5M2, flags, flags ? n_flags : 0, given};
   CUtensorMap tx, tw;
   cudaError_t e = make_map_2d(&tw, W, desc->d_out, desc->d_in, 1, 128);
   if (e != cudaSuccess) return cuda_status(e, where);
@@ -380,7 +409,7 @@ dora_status_t product(bool backward, const dora_fp8_desc_t* desc, int64_t T, con
                    : launch_narrow<16, false, float>(tw, tw, g, false, st);
     return cuda_status(e, where);
   }
-  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   const bool narrow = p.narrow;
   e = make_map_2d(&tx, xq, T, K, 1, narrow ? nt : 128);
   if (e == cudaSuccess) {

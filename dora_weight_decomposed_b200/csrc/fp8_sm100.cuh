@@ -121,6 +121,7 @@ struct Fp8Geom {
   // scales are applied in fp32.
   const int* flags;
   int n_flags;
+  int xs_given;  // x's scales come from the caller and may be no powers of two
 };
 
 // A scale that the tensor cores can apply: a positive normal power of two; or a non-finite scale of x, which stands for
@@ -153,21 +154,26 @@ __device__ __forceinline__ void fma2(float2& a, uint32_t v0, uint32_t v1, float 
 // ------------------------------------------------------------------ few tokens
 //
 // With few tokens the weight's bytes are the cost, so the operands change places: 128 rows of the weight are the
-// MMA's M, NT tokens its N (64 at most: T = 128 of 8192 x 8192 takes 28.9 us in two tiles of 64 tokens and 33.5 in
-// one of 128, whose folding is the longer chain), and D holds the result transposed (lane = weight row, column = token). The K
+// MMA's M, NT tokens its N, and D holds the result transposed (lane = weight row, column = token). The K
 // blocks of a tile are split over the CTAs of a cluster so that enough of the weight is in flight on every SM; two
-// CTAs fit on one SM. Each CTA folds its k-blocks into registers; the cluster then adds the splits
+// CTAs fit on one SM. Where the CTA's scales are powers of two the tensor cores apply them (see the CTA pairs below)
+// and add up all of its k-blocks; else each k-block is folded into registers (T = 100 of 27648 x 5120: 32 against 55 us,
+// T = 128 of 8192 x 8192: 21.5 against 29; T = 37 of 27648 x 5120, where the weight's bytes are 22 us: 28.5 against 29.6).
+// The cluster then adds the splits
 // through distributed shared memory in rank order, so the result does not depend on timing.
 // W_MN: the weight's rows run along K (the input gradient, W [d_out x d_in] with K = d_out).
 template <int NT>
 struct Fp8Narrow {
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = 16384 + X_BYTES;
-  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4;
+  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
   static constexpr int SCALE_BYTES = 8 * NT * 4;  // token scales: two k-blocks per folding warp, or one per stage
   static_assert(STAGES <= 8, "scales");
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES + 256 + 1024;
-  static constexpr uint32_t ACC_COLS = NT < 32 ? 16 : NT;  // two accumulators; TMEM comes in 32 columns at least
+  // TMEM: two accumulators of k-blocks, or one for all of them and 8 columns of scales per stage.
+  static constexpr uint32_t ACC_COLS = NT;
+  static constexpr uint32_t USED = 2 * NT > NT + 8 * STAGES ? 2 * NT : NT + 8 * STAGES;
+  static constexpr uint32_t TMEM_COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : 256;
   static_assert(NT * 128 * 4 <= STAGES * STAGE_BYTES, "the splits' sums fit the ring");
   static_assert(SMEM_BYTES + 1024 <= 114 * 1024, "two CTAs per SM");
 };
@@ -215,7 +221,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;  // [2] accumulator complete
   uint64_t* acce = accf + 2;        // [2] accumulator folded
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+  uint64_t* sff = acce + 2;         // [STAGES] a k-block's scales are in TMEM
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sff + STAGES);
 
   constexpr bool OWN_X = !std::is_same<XT, void>::value;
   const int warp = threadIdx.x >> 5;
@@ -230,6 +237,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], OWN_X ? 5 : 1);  // the loads, and the four warps that write x
       mbar_init(&empty[s], 1);
+      mbar_init(&sff[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     if (!OWN_X) prefetch_tmap(&tX);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 2 * Cfg::ACC_COLS);
+    tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -250,23 +258,43 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   pdl_trigger();
   if (!early_w) pdl_wait();
 
+  const float* ws = g.ws + (size_t)(n0 >> 7) * g.ws_n + (size_t)kb0 * g.ws_k;
+  // The weight does not come from the preceding grid (the quantisation of x): its first stages are under way before
+  // that grid is done.
+  auto load_w = [&](int i) {
+    uint8_t* sw = smem + i % STAGES * Cfg::STAGE_BYTES;
+    mbar_arrive_expect_tx(&full[i % STAGES], OWN_X ? 16384 : Cfg::STAGE_BYTES);
+    if (!W_MN)
+      tma_load_2d(sw, &tW, &full[i % STAGES], (kb0 + i) * kF8BK, n0);
+    else
+      tma_load_2d(sw, &tW, &full[i % STAGES], n0, (kb0 + i) * kF8BK);
+  };
+  const int ahead = min(nkb, STAGES);
+  if (warp == 0 && lane == 0)
+    for (int i = 0; i < ahead; ++i) load_w(i);
+  // The tensor cores apply the scales where every one is a power of two. A call that may quantise x itself folds
+  // (T = 1 of 4096 x 4096: 7.2 us, and 7.8 if its scales are looked at first), with given codes too: the same sums.
+  bool mx = !OWN_X && (NT > 16 || per > STAGES);
+  if constexpr (!OWN_X) {
+    mx = mx && (!g.out_fp32 || nkb <= kF8MaxBlocksFp32);
+    if (warp >= 2) {  // this CTA's scales (those of an x quantised in the call are powers of two by their making)
+      const int tid = threadIdx.x - 64;
+      for (int i = tid; i < nkb; i += 128) mx = mx && is_power(ws[(size_t)i * g.ws_k]);
+      if (g.xs_given) {
+        for (int i = tid; i < nkb * NT; i += 128) {
+          const int t = t0 + i % NT;
+          mx = mx && (t >= g.T || is_power_or_bad(g.xs[(size_t)(kb0 + i / NT) * g.T + t]));
+        }
+      }
+    }
+    mx = __syncthreads_and(mx);
+  }
+
   float2 acc[NT / 2];
 #pragma unroll
   for (int t = 0; t < NT / 2; ++t) acc[t] = make_float2(0.f, 0.f);
   if (warp == 0) {
     if (lane == 0) {
-      // The weight does not come from the preceding grid (the quantisation of x): its first stages are under way
-      // before that grid is done.
-      auto load_w = [&](int i) {
-        uint8_t* sw = smem + i % STAGES * Cfg::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[i % STAGES], OWN_X ? 16384 : Cfg::STAGE_BYTES);
-        if (!W_MN)
-          tma_load_2d(sw, &tW, &full[i % STAGES], (kb0 + i) * kF8BK, n0);
-        else
-          tma_load_2d(sw, &tW, &full[i % STAGES], n0, (kb0 + i) * kF8BK);
-      };
-      const int ahead = early_w ? min(nkb, STAGES) : 0;
-      for (int i = 0; i < ahead; ++i) load_w(i);
       if (early_w) pdl_wait();
       int i = 0;
 #pragma unroll 1
@@ -283,10 +311,31 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_fp8_f32(128, NT, false, g.a_e5m2 != 0, false) | (W_MN ? 1u << 15 : 0u);
+      const uint32_t idesc = (mx ? idesc_mxfp8(128, NT, false, g.a_e5m2 != 0, false)
+                                 : idesc_fp8_f32(128, NT, false, g.a_e5m2 != 0, false)) | (W_MN ? 1u << 15 : 0u);
       constexpr uint32_t w_kstep = W_MN ? 32u * 128u : 32u;
+      if (mx) {
+        bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < nkb; ++i) {
+        for (int i = 0; i < nkb; ++i) {
+          const int s = i % STAGES;
+          const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
+          if (!mbar_wait(&sff[s], ph) || !mbar_wait(&full[s], ph)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sw = smem_u32(smem + s * Cfg::STAGE_BYTES), sf = tmem + NT + 8u * s;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxfp8(tmem, sdesc_sw128(sw + kk * w_kstep, 16u, 1024u), sdesc_sw128(sw + 16384u + kk * 32u, 16u, 1024u), idesc,
+                       sf, sf + 4u, i > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(&empty[s]);
+        }
+        if (ok) umma_commit(accf);
+      }
+#pragma unroll 1
+      for (int i = mx ? nkb : 0; i < nkb; ++i) {
         const int s = i % STAGES, b = i & 1;
         if (!mbar_wait(&acce[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) break;
         if (!mbar_wait(&full[s], (uint32_t)(i / STAGES) & 1u)) break;
@@ -303,7 +352,31 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   } else {
     if (early_w) pdl_wait();
     const int q = warp & 3;
-    const float* ws = g.ws + (size_t)(n0 >> 7) * g.ws_n + (size_t)kb0 * g.ws_k;
+    // Scales of block i into TMEM: x's exponent bytes (xs[c]: of token 32 c + lane) and the weight's one.
+    auto put_scales = [&](int i, const float (&xs)[4], float w) {
+      const auto word = [](float s) { return (__float_as_uint(s) >> 23 & 0xffu) * 0x01010101u; };
+      const uint32_t col = tmem + NT + 8u * (i % STAGES) + ((uint32_t)(q * 32) << 16), a = word(w);
+      tc_fence_after();
+      tmem_st4(col, a, a, a, a);
+      tmem_st4(col + 4, word(xs[0]), word(xs[1]), word(xs[2]), word(xs[3]));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sff[i % STAGES]);
+    };
+    // The whole sum, once the last block's MMAs are done.
+    auto read_sum = [&]() {
+      if (nkb == 0 || !mbar_wait(accf, 0)) return;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld16_async(tmem + c * 16 + ((uint32_t)(q * 32) << 16), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[8 * c + j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+      }
+    };
     auto fold = [&](int b, const float* sc) {
       const uint32_t ta = tmem + b * Cfg::ACC_COLS + ((uint32_t)(q * 32) << 16);
 #pragma unroll
@@ -373,6 +446,36 @@ __global__ void __launch_bounds__(kF8Threads, 2)
         tc_fence_after();
         fold(i & 1, scales + i * NT);
       }
+    } else if (mx) {
+      // Scales are fetched four k-blocks ahead, without a move that would wait for them.
+      float v[4][4], wv[4];
+      auto fetch = [&](int i, float (&x4)[4], float& w) {
+        if (i >= nkb) return;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int t = t0 + 32 * c + lane;
+          x4[c] = 32 * c < NT && t < g.T ? g.xs[(size_t)(kb0 + i) * g.T + t] : 0.f;
+        }
+        w = ws[(size_t)i * g.ws_k];
+      };
+      bool ok = true;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) fetch(u, v[u], wv[u]);
+#pragma unroll 1
+      for (int i4 = 0; i4 < nkb && ok; i4 += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i4 + u;
+          if (i >= nkb) break;
+          if (!mbar_wait(&empty[i % STAGES], ((uint32_t)(i / STAGES) & 1u) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          put_scales(i, v[u], wv[u]);
+          fetch(i + 4, v[u], wv[u]);
+        }
+      }
+      if (ok) read_sum();
     } else {
       constexpr int NS = (NT + 31) / 32;
       // Lane l fetches the scales of tokens l, l + 32, ... one k-block ahead; every lane reads them back from the warp's
@@ -437,7 +540,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * Cfg::ACC_COLS);
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
   }
 }
 

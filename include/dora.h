@@ -260,9 +260,11 @@ DORA_API dora_status_t dora_merge(const dora_desc_t* desc, const void* W0, const
  *     dx[t][k] = sum_nb dy_scale[nb][t] w_scale[nb][k / 128] sum_{n in nb} dyq[t][n] wq[n][k]
  *   Sums are fp32; each result is rounded once to out_dtype (bf16 or fp32).
  *   Products of 128 values are added in the tensor cores' accumulator and
- *   those sums, scaled, in fp32; above 128 tokens, if every scale is a power of
- *   two, bf16 results (fp32 ones up to 4096 values) are added in the tensor
- *   cores whole, whose additions round a little worse than fp32's.
+ *   those sums, scaled, in fp32; where scales are powers of two, bf16 results
+ *   (and sums of up to 4096 values for fp32 ones) may be added in the tensor
+ *   cores whole, whose additions round a little worse than fp32's. How a sum
+ *   is split depends on T and the device, so the same row in batches of other
+ *   sizes can differ in its last bits; a call repeated gives the same bits.
  *   in_dtype bf16 or fp32: the operand is quantised in the call to fp8_dtype
  *   in 1 x 128 blocks (x_scale must be NULL). in_dtype e4m3 or e5m2: it comes
  *   quantised, with the scales of DORA_FP8_ROWS (fp8_dtype is not read).

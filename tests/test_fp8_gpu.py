@@ -6,10 +6,10 @@ the oracle's. Products: with a_tk = |x_scale xq|, b_nk = |w_scale wq| the sum of
 128 * 2^-23 of the block's sum of |products| (one unit in the last place per
 addition, rounded or cut off), and folding nkb blocks with a rounded scale by at most
 (nkb + 3) * 2^-24 of the whole; the result is then rounded once, by at most
-half a step of the output type. Above 128 tokens, when every scale is a power of
-two, the tensor core applies the scales (exactly) and adds all K products of a
-result in the one accumulator: then the first bound is K * 2^-23 of the sum of
-|products|. If those K roundings are independent, their sum is off by about
+half a step of the output type. Where the scales of a tile are powers of two,
+the tensor core may apply them (exactly) and add all K products of a result in
+the one accumulator: then the first bound is K * 2^-23 of the sum of |products|.
+If those K roundings are independent, their sum is off by about
 sqrt(K) * 2^-24 of the largest partial sum, so the whole matrix is also held to
 sqrt(K) * 2^-22 of its norm (and the output's rounding).
 """
@@ -110,9 +110,9 @@ def weight(d_out, d_in, seed=1, pow2=False):
 
 
 def check_product(out, a, b, K, what="", powers=False):
-    """out against a @ b (float64), by the bounds of the module's first lines; powers: every scale is a power of two."""
+    """out against a @ b (float64), by the bounds of the module's first lines; powers: scales that are powers of two."""
     ref, mag = a @ b, np.abs(a) @ np.abs(b)
-    sums = K if powers and len(a) > 128 else 128
+    sums = K if powers else 128
     tol = (sums * 2.0 ** -23 + (-(-K // 128) + 3) * 2.0 ** -24) * mag
     if not np.isnan(ref).any():
         far = np.linalg.norm(host(out) - ref) / max(np.linalg.norm(ref), 1e-300)
@@ -172,7 +172,8 @@ def test_products_of_wide_operands(T, d_out, d_in, dtype, backward):
 
 
 @pytest.mark.parametrize("backward", [False, True])
-@pytest.mark.parametrize("T,d_out,d_in", [(129, 256, 128), (256, 272, 1168), (300, 528, 400), (517, 1040, 272), (140, 144, 27648)])
+@pytest.mark.parametrize("T,d_out,d_in", [(129, 256, 128), (256, 272, 1168), (300, 528, 400), (517, 1040, 272), (140, 144, 27648),
+                                           (17, 400, 528), (70, 1040, 2064), (128, 272, 272), (16, 144, 27648)])
 def test_scales_that_are_powers_of_two_and_others(T, d_out, d_in, backward):
     """The tensor cores apply the scales of the first call; one scale of the weight, or of the operand, in the later ones
     is no power of two, zero, negative or subnormal, and those are applied in fp32."""
@@ -193,11 +194,11 @@ def test_scales_that_are_powers_of_two_and_others(T, d_out, d_in, backward):
             xs.view(-1)[xs.numel() // 2] = v
         out = fn(xq, wq, ws, out_dtype=torch.float32, **{key: xs})
         w = of.widen_tiles(host(wq), host(ws))
-        check_product(out, of.widen_rows(host(xq), host(xs)), w if backward else w.T, K, what, powers=what == "powers")
+        check_product(out, of.widen_rows(host(xq), host(xs)), w if backward else w.T, K, what, powers=True)  # those of other tiles stay
 
 
 @pytest.mark.parametrize("pow2", [False, True])
-@pytest.mark.parametrize("T", [1, 9, 140, 300])
+@pytest.mark.parametrize("T", [1, 9, 24, 100, 140, 300])
 def test_non_finite_rows_stay_in_their_rows(T, pow2):
     x = matrix(T, 384, torch.bfloat16, wide=False)
     wq, ws = weight(272, 384, pow2=pow2)
@@ -242,7 +243,7 @@ def test_gradient_by_differences(T):
     w = of.widen_tiles(host(wq), host(ws))
     # three results, each an fp32 sum within the products' bound of its sum of magnitudes (|x| <= 15 here)
     mag = float((np.abs(host(dy)) @ np.abs(w)).sum()) * 15 * 2 + float((np.abs(host(dy)) @ np.abs(w) * np.abs(host(dirn))).sum())
-    sums = 400 if T > 128 else 128  # products added in one accumulator (d_in = 400, d_out = 272)
+    sums = 400  # products added in one accumulator at most (d_in = 400, d_out = 272)
     assert abs(diff - want) <= (sums * 2.0 ** -23 + 10 * 2.0 ** -24) * mag
 
 
