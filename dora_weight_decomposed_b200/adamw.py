@@ -176,7 +176,7 @@ class DoraAdamW:
         if max_norm is not None:
             if grad_scale is not None:
                 raise ValueError("give max_norm or grad_scale, not both")
-            norm = _empty((), torch.float32, device, stream)
+            norm = self._lr.new_empty(()) if stream is None else _empty((), torch.float32, device, stream)
             _check(lib.dora_adamw_clipped(self._ref, self._tensors, self._n, self._control_ptr, max_norm, norm.data_ptr(),
                                           self._ws_ptr, self._ws_bytes, _stream(stream, device)))
             return norm

@@ -173,43 +173,58 @@ cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
-// answer of the occupancy query, which counts one CTA per SM for the narrow kernels; asked once per device.
-template <int NT, bool W_MN>
-int clusters_alone(int cs) {
-  static std::atomic<int> known[64][9];
+// The current device, for what is asked once per device (63: none, or any behind it), and its SMs.
+int this_device() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) dev = 63;
-  int n = known[dev][cs].load();
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cs * 1024u);
-    cfg.blockDim = dim3(kF8Threads);
-    cfg.dynamicSmemBytes = Fp8Narrow<NT>::SMEM_BYTES;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cs;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, void>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = std::max(1, device_sm_count() / cs * 7 / 8);
-    }
-    n = std::min(n, std::max(1, device_sm_count() / cs));
-    known[dev][cs].store(n);
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 63;
   }
+  return std::min(dev, 63);
+}
+int sm_count(int dev) {
+  static std::atomic<int> known[64];
+  int n = known[dev].load();
+  if (n == 0) known[dev].store(n = device_sm_count());
   return n;
+}
+
+// Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
+// answer of the occupancy query, which counts one CTA per SM for the narrow kernels.
+template <int NT, bool W_MN>
+int clusters_alone(int cs, int sms) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cs * 1024u);
+  cfg.blockDim = dim3(kF8Threads);
+  cfg.dynamicSmemBytes = Fp8Narrow<NT>::SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, void>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = std::max(1, sms / cs * 7 / 8);
+  }
+  return std::min(n, std::max(1, sms / cs));
 }
 
 // The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two): twice as
 // many. Seen in the times: 48 tiles in one wave with 5 splits and in two with 6, 96 tiles with 2 and 3. The small CTAs of
 // 16 tokens also fit as one cluster on every (cs + 1) / 2 SMs: 32 tiles with 8 splits in one wave, which at 128 tokens
-// (256 x 2048 x 2048) took 12.2 us, and 9.5 with 6.
+// (256 x 2048 x 2048) took 12.2 us, and 9.5 with 6. slots[cs], asked for once per device.
 template <int NT, bool W_MN>
-int narrow_slots(int cs) {
-  const int twice = 2 * clusters_alone<NT, W_MN>(cs);
-  return NT == 16 ? std::max(twice, clusters_alone<NT, W_MN>((cs + 1) / 2)) : twice;
+const int* narrow_slots(int dev) {
+  static std::once_flag once[64];
+  static int slots[64][9];
+  std::call_once(once[dev], [&] {
+    int alone[9];
+    for (int cs = 1; cs <= 8; ++cs) alone[cs] = clusters_alone<NT, W_MN>(cs, sm_count(dev));
+    for (int cs = 1; cs <= 8; ++cs) slots[dev][cs] = std::max(2 * alone[cs], NT == 16 ? alone[(cs + 1) / 2] : 0);
+  });
+  return slots[dev];
 }
 
 // CTAs per tile of the narrow kernel (K splits, one cluster) and the call's estimated time in microseconds: waves of
@@ -223,12 +238,13 @@ struct NarrowChoice {
   double us = 1e300;
 };
 template <int NT, bool W_MN>
-NarrowChoice narrow_choice(int64_t tiles, int64_t nkb, int64_t least = 1) {
+NarrowChoice narrow_choice(int dev, int64_t tiles, int64_t nkb, int64_t least = 1) {
   NarrowChoice best;
-  const int sms = device_sm_count();
+  const int sms = sm_count(dev);
+  const int* slots = narrow_slots<NT, W_MN>(dev);
   for (int cs = (int)least; cs <= 8 && cs <= nkb; ++cs) {
     const double block = tiles * cs > sms ? 0.6 : 0.43, add = cs > 1 ? 2.0 + NT / 64.0 : 0.0;
-    const int64_t waves = cdiv(tiles, narrow_slots<NT, W_MN>(cs));
+    const int64_t waves = cdiv(tiles, slots[cs]);
     const double us = (double)waves * ((double)cdiv(nkb, cs) * block + add + 1.0) + 4.0;
     if (us < best.us - 1e-9) {
       best.us = us;
@@ -241,14 +257,14 @@ NarrowChoice narrow_choice(int64_t tiles, int64_t nkb, int64_t least = 1) {
 // The least number of splits that leaves a CTA no more k-blocks than the ring's stages, so that the kernel can quantise x
 // itself, or 0 where the device's 2 CTAs per SM do not allow as many. Not by what clusters fit: those differ from one
 // device to the next, and a workspace asked for on one of them has to do on another.
-int64_t few_blocks_splits(int64_t T, int64_t N, int64_t nkb) {
-  const int64_t most = std::clamp<int64_t>(2 * device_sm_count() / cdiv(N, 128), 1, 8), least = cdiv(nkb, Fp8Narrow<16>::STAGES);
+int64_t few_blocks_splits(int dev, int64_t T, int64_t N, int64_t nkb) {
+  const int64_t most = std::clamp<int64_t>(2 * sm_count(dev) / cdiv(N, 128), 1, 8), least = cdiv(nkb, Fp8Narrow<16>::STAGES);
   return T <= 16 && least <= most ? least : 0;
 }
 
 // The pair kernel's time: waves of 256 x 256 tiles, 0.44 us per k-block, up to 0.56 with every pair busy, plus 6.
-double pair_us(int64_t T, int64_t N, int64_t nkb) {
-  const int64_t pairs = std::max(1, device_sm_count() / 2), tiles = cdiv(T, 256) * cdiv(N, 256);
+double pair_us(int dev, int64_t T, int64_t N, int64_t nkb) {
+  const int64_t pairs = std::max(1, sm_count(dev) / 2), tiles = cdiv(T, 256) * cdiv(N, 256);
   return (double)cdiv(tiles, pairs) * (double)nkb * (0.44 + 0.12 * (double)std::min(tiles, pairs) / (double)pairs) + 6.0;
 }
 
@@ -260,7 +276,8 @@ cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
   // (The same splits for an x that comes in codes as for one that is quantised here: the same sums.)
-  const int cs = narrow_choice<NT, W_MN>(tiles * t_tiles, g.nkb, std::max<int64_t>(1, few_blocks_splits(g.T, g.N, g.nkb))).cs;
+  const int dev = this_device();
+  const int cs = narrow_choice<NT, W_MN>(dev, tiles * t_tiles, g.nkb, std::max<int64_t>(1, few_blocks_splits(dev, g.T, g.N, g.nkb))).cs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * t_tiles * cs));
   cfg.blockDim = dim3(kF8Threads);
@@ -304,7 +321,7 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs < kF8LaunchRegs) return cudaErrorInvalidKernelImage;
-  const int64_t pairs = std::min<int64_t>(cdiv(g.T, 256) * cdiv(g.N, 256), std::max(1, device_sm_count() / 2));
+  const int64_t pairs = std::min<int64_t>(cdiv(g.T, 256) * cdiv(g.N, 256), std::max(1, sm_count(this_device()) / 2));
   ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
   return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, tout, g);
 }
@@ -323,18 +340,19 @@ Fp8Plan fp8_plan(const dora_fp8_desc_t& d, int64_t T, int op) {
   const bool back = op == DORA_FP8_OP_BACKWARD;
   const int64_t K = back ? d.d_out : d.d_in, N = back ? d.d_in : d.d_out, nkb = cdiv(K, 128);
   if (T == 0) return p;
+  const int dev = this_device();
   // Tiles of up to 128 tokens with K split over clusters, or 256 x 256 tiles on CTA pairs: the latter need many
   // tiles (T = 512: 1024 x 8192 20 us narrow and 34 us on pairs, 4096 x 4096 18.4 and 21.1, 8192 x 8192 43.3 and 42.1,
   // 6144 x 2048 15.9 and 15.0).
   if (T > 128) {
     const int64_t tiles = cdiv(N, 128) * cdiv(T, 128);
-    const double us = back ? narrow_choice<128, true>(tiles, nkb).us : narrow_choice<128, false>(tiles, nkb).us;
-    p.narrow = us < pair_us(T, N, nkb);
+    const double us = back ? narrow_choice<128, true>(dev, tiles, nkb).us : narrow_choice<128, false>(dev, tiles, nkb).us;
+    p.narrow = us < pair_us(dev, T, N, nkb);
   }
   p.flags = !p.narrow && (d.out_dtype == DORA_BF16 || nkb <= kF8MaxBlocksFp32);
   if (T > 128) p.total = kF8MaxFlags * sizeof(int);  // the choice may differ between devices, the workspace may not
   if (is_fp8(d.in_dtype)) return p;
-  p.own_x = few_blocks_splits(T, N, nkb) > 0;
+  p.own_x = few_blocks_splits(dev, T, N, nkb) > 0;
   if (p.own_x) return p;
   p.off_q = p.total;
   p.off_s = p.off_q + align256((size_t)T * K);

@@ -59,14 +59,16 @@ def _tensor(t, shape, dtype, device, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-_current_device = None  # torch.cuda.current_device, set on first use
+_current_device = None  # index of the current device: torch.cuda.current_device, or what it calls, set on first use
 
 
 def _current(device) -> None:
     global _current_device
     if device.type == "cuda":
         if _current_device is None:
-            _current_device = _torch().cuda.current_device
+            torch = _torch()
+            torch.cuda.current_device()  # CUDA is initialised from here on
+            _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         if device.index != _current_device():
             raise ValueError(f"tensors are on {device}, but the current device is cuda:{_current_device()}; "
                              f"call under torch.cuda.device({device.index})")
@@ -200,9 +202,11 @@ def _product(op: int, x, wq, w_scale, x_scale, out, out_dtype, fp8_dtype, ws, st
         _tensor(out, shape, out_dtype, dev, "y" if op == DORA_FP8_OP_FORWARD else "dx")
     nbytes = need
     if ws is not None:
+        if ws.device != dev:
+            raise ValueError(f"ws is on {ws.device}, expected {dev}")
         nbytes = ws.numel() * ws.element_size()
     elif need:
-        ws = _empty(need, _torch().uint8, dev, stream)
+        ws = w_scale.new_empty(-(-need // 4)) if stream is None else _empty(need, _torch().uint8, dev, stream)
     if x.is_cuda and x.is_contiguous() and wq.is_contiguous() and w_scale.is_contiguous():  # all on one device, by the plan
         status = call(ref, shape[0], x.data_ptr(), _ptr(x_scale), wq.data_ptr(), w_scale.data_ptr(), _ptr(out), _ptr(ws),
                       nbytes, _stream(stream, dev))

@@ -270,7 +270,8 @@ DORA_API dora_status_t dora_merge(const dora_desc_t* desc, const void* W0, const
  *   quantised, with the scales of DORA_FP8_ROWS (fp8_dtype is not read).
  *   Any fp32 scales are taken, not only powers of two. W is e4m3 [d_out x
  *   d_in] with the scales of DORA_FP8_TILES. d_out and d_in are multiples of
- *   16; T may be any value >= 0 (T = 0 does nothing).
+ *   16; T may be any value >= 0 (T = 0 does nothing). y or dx must not
+ *   overlap the other tensors, nor q and scale the matrix they are made of.
  *   Workspace: dora_fp8_workspace_size (0 for an invalid descriptor).
  */
 typedef enum { DORA_FP8_ROWS = 0, DORA_FP8_TILES = 1 } dora_fp8_block_t;

@@ -293,6 +293,8 @@ def test_refusals_on_the_device():
     x = matrix(4, 128, torch.bfloat16)
     with pytest.raises(dw.DoraError, match="EWORKSPACE"):
         dw.dora_fp8_forward(matrix(20, 128, torch.bfloat16), wq, ws, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        dw.dora_fp8_forward(matrix(20, 128, torch.bfloat16), wq, ws, ws=torch.empty(1 << 16, dtype=torch.uint8))
     with pytest.raises(ValueError, match="contiguous"):
         dw.dora_fp8_forward(matrix(4, 256, torch.bfloat16)[:, :128], wq, ws)
     buf = torch.zeros(4 * 128 + 4, dtype=torch.bfloat16, device="cuda")
