@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -257,8 +258,8 @@ template <int MAX>
 __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __grid_constant__ GradTable<MAX> t,
                                                                      double* __restrict__ part) {
   __shared__ double red[kThreads / 32];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // only now: the update that follows reads the parameters and moments ahead of this grid's end
   double sum = 0.0;
   const Range range = cta_range(t.chunks);
   for (int c = range.first, k = find_tensor(t, range.first); c < range.last; ++k) {
@@ -430,6 +431,16 @@ __device__ __forceinline__ void load_elements(const AdamEntry& e, int64_t i, Ele
   }
 }
 
+// Elements i .. i + 7 of tensor e into L2 (32 bits; held in registers over the wait they would spill).
+__device__ __forceinline__ void prefetch_elements(const AdamEntry& e, int64_t i) {
+  if (i >= e.n) return;
+  const auto fetch = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+  fetch((const char*)e.g + i * (e.g_fp32 ? 4 : 2));
+  fetch(e.master ? (const char*)(e.master + i) : (const char*)e.p + i * (e.p_fp32 ? 4 : 2));
+  fetch((const float*)e.avg + i);
+  fetch((const float*)e.sq + i);
+}
+
 // The update of elements i .. i + 7 of tensor e by one thread; the warp's lanes hold consecutive ones. WHOLE: the
 // elements lie in a whole chunk of an aligned tensor.
 template <int BITS, bool WHOLE>
@@ -543,65 +554,63 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <int MAX>
-__device__ __forceinline__ void update_range_staged(const AdamTable<MAX>& t, const AdamArgs& a, const StepScalars& sc,
-                                                    const Range range) {
-  __shared__ Stage8 stage[2];
-  __shared__ uint64_t full[2];
-  if (threadIdx.x == 0) {
-    mbar_init(&full[0], 1);
-    mbar_init(&full[1], 1);
-    fence_mbar_init();
+struct Stages {
+  Stage8 stage[2];
+  uint64_t full[2];
+};
+
+__device__ __forceinline__ bool is_whole(const AdamEntry& e, int64_t i0) { return e.bulk && i0 + kChunk <= e.n; }
+
+// Chunk c of tensor e, which starts at chunk e_first, into stage b (one thread): bulk copies, or an empty phase.
+__device__ __forceinline__ void issue_chunk(Stages& s, int b, const AdamEntry& e, int e_first, int c) {
+  const int64_t i0 = (int64_t)(c - e_first) * kChunk;
+  Stage8& to = s.stage[b];
+  uint64_t* bar = &s.full[b];
+  if (!is_whole(e, i0)) {
+    mbar_arrive(bar);
+    return;
   }
-  __syncthreads();
-  const auto whole = [](const AdamEntry& e, int64_t i0) { return e.bulk && i0 + kChunk <= e.n; };
-  // Chunk c of tensor k into its stage (thread 0): bulk copies, or an empty phase.
-  auto issue = [&](int c, int k) {
-    const AdamEntry& e = t.e[k];
-    const int64_t i0 = (int64_t)(c - t.first[k]) * kChunk;
-    Stage8& s = stage[(c - range.first) & 1];
-    uint64_t* bar = &full[(c - range.first) & 1];
-    if (!whole(e, i0)) {
-      mbar_arrive(bar);
-      return;
-    }
-    const uint32_t gb = e.g_fp32 ? 4 : 2, pb = e.master || e.p_fp32 ? 4 : 2;
-    const char* p = e.master ? (const char*)e.master : (const char*)e.p;
-    mbar_arrive_expect_tx(bar, kChunk * (gb + pb + 2) + 2 * kChunk / 128 * 4);
-    bulk_load(s.g, (const char*)e.g + i0 * gb, kChunk * gb, bar);
-    bulk_load(s.p, p + i0 * pb, kChunk * pb, bar);
-    bulk_load(s.cm, (const char*)e.avg + i0, kChunk, bar);
-    bulk_load(s.cv, (const char*)e.sq + i0, kChunk, bar);
-    bulk_load(s.sm, e.savg + (i0 >> 7), kChunk / 128 * 4, bar);
-    bulk_load(s.sr, e.ssq + (i0 >> 7), kChunk / 128 * 4, bar);
-  };
-  int k = find_tensor(t, range.first), kn = k;
-  if (threadIdx.x == 0) issue(range.first, k);
+  const uint32_t gb = e.g_fp32 ? 4 : 2, pb = e.master || e.p_fp32 ? 4 : 2;
+  const char* p = e.master ? (const char*)e.master : (const char*)e.p;
+  mbar_arrive_expect_tx(bar, kChunk * (gb + pb + 2) + 2 * kChunk / 128 * 4);
+  bulk_load(to.g, (const char*)e.g + i0 * gb, kChunk * gb, bar);
+  bulk_load(to.p, p + i0 * pb, kChunk * pb, bar);
+  bulk_load(to.cm, (const char*)e.avg + i0, kChunk, bar);
+  bulk_load(to.cv, (const char*)e.sq + i0, kChunk, bar);
+  bulk_load(to.sm, e.savg + (i0 >> 7), kChunk / 128 * 4, bar);
+  bulk_load(to.sr, e.ssq + (i0 >> 7), kChunk / 128 * 4, bar);
+}
+
+// The CTA's chunks, the first of which (of tensor k) has been issued.
+template <int MAX>
+__device__ __forceinline__ void update_range_staged(Stages& s, const AdamTable<MAX>& t, const AdamArgs& a,
+                                                    const StepScalars& sc, const Range range, int k) {
+  int kn = k;
   bool ok = true;
 #pragma unroll 1
   for (int c = range.first; c < range.last; ++c) {
     const int it = c - range.first;
     if (c + 1 < range.last) {
       while (kn + 1 < t.n && t.first[kn + 1] <= c + 1) ++kn;
-      if (threadIdx.x == 0) issue(c + 1, kn);
+      if (threadIdx.x == 0) issue_chunk(s, (it + 1) & 1, t.e[kn], t.first[kn], c + 1);
     }
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[it & 1], (uint32_t)(it >> 1) & 1u));
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(&s.full[it & 1], (uint32_t)(it >> 1) & 1u));
     if (ok) {  // a wait that ran out leaves the rest of the warp's elements as they are
       const AdamEntry& e = t.e[k];
       const int64_t i0 = (int64_t)(c - t.first[k]) * kChunk, i = i0 + threadIdx.x * 8;
       Elements<8> x;
-      if (whole(e, i0)) {
-        const Stage8& s = stage[it & 1];
-        const uint4* g = reinterpret_cast<const uint4*>(s.g) + threadIdx.x * (e.g_fp32 ? 2 : 1);
-        const uint4* p = reinterpret_cast<const uint4*>(s.p) + threadIdx.x * (e.master || e.p_fp32 ? 2 : 1);
+      if (is_whole(e, i0)) {
+        const Stage8& st = s.stage[it & 1];
+        const uint4* g = reinterpret_cast<const uint4*>(st.g) + threadIdx.x * (e.g_fp32 ? 2 : 1);
+        const uint4* p = reinterpret_cast<const uint4*>(st.p) + threadIdx.x * (e.master || e.p_fp32 ? 2 : 1);
         x.g.a = g[0];
         x.p.a = p[0];
         if (e.g_fp32) x.g.b = g[1];
         if (e.master || e.p_fp32) x.p.b = p[1];
-        x.cm = reinterpret_cast<const uint2*>(s.cm)[threadIdx.x];
-        x.cv = reinterpret_cast<const uint2*>(s.cv)[threadIdx.x];
-        x.sm = s.sm[threadIdx.x >> 4];
-        x.sr = s.sr[threadIdx.x >> 4];
+        x.cm = reinterpret_cast<const uint2*>(st.cm)[threadIdx.x];
+        x.cv = reinterpret_cast<const uint2*>(st.cv)[threadIdx.x];
+        x.sm = st.sm[threadIdx.x >> 4];
+        x.sr = st.sr[threadIdx.x >> 4];
         update<8, true>(e, a, sc, i, x);
       } else {
         load_elements<8>(e, i, x);
@@ -613,36 +622,54 @@ __device__ __forceinline__ void update_range_staged(const AdamTable<MAX>& t, con
   }
   if (!ok && threadIdx.x == 0) {  // let the last copies land before the shared memory goes
     const int last = range.last - 1 - range.first;
-    mbar_wait(&full[last & 1], (uint32_t)(last >> 1) & 1u, kWaitLimitNs / 16);
+    mbar_wait(&s.full[last & 1], (uint32_t)(last >> 1) & 1u, kWaitLimitNs / 16);
   }
 }
 
+// early: the grid before this one is the gradient norm's, which starts only when all work before it is done and writes
+// its partial sums alone. So the first chunk is read while that grid runs.
 template <int BITS, int MAX>
 __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamTable<MAX> t, const AdamArgs a,
                                                             dora_adamw_control_t* __restrict__ control,
-                                                            const float* __restrict__ grad_scale, int last) {
+                                                            const float* __restrict__ grad_scale, int early, int last) {
   pdl_trigger();
-  pdl_wait();
+  if (!early) pdl_wait();
+  const Range range = cta_range(t.chunks);
+  const bool any = range.first < range.last;
+  const int k0 = any ? find_tensor(t, range.first) : 0;
+  const int64_t i0 = any ? (int64_t)(range.first - t.first[k0]) * kChunk + threadIdx.x * 8 : 0;
+  __shared__ typename std::conditional<BITS == 8, Stages, int>::type stages;
+  if constexpr (BITS == 8) {
+    if (threadIdx.x == 0) {
+      mbar_init(&stages.full[0], 1);
+      mbar_init(&stages.full[1], 1);
+      fence_mbar_init();
+      if (any) issue_chunk(stages, 0, t.e[k0], t.first[k0], range.first);
+    }
+    __syncthreads();
+  } else if (early && any) {
+    prefetch_elements(t.e[k0], i0);
+  }
   const int64_t step = control->step + 1;
   StepScalars sc;
   sc.lr = control->lr;
   sc.gs = grad_scale ? *grad_scale : 1.0f;
+  if (early) pdl_wait();
   if (a.part) {
     const NormScale r = norm_and_scale(a.part, a.parts, a.max_norm);
     sc.gs = r.scale;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)r.norm;
   }
   const bool run = isfinite(sc.gs);
-  const Range range = cta_range(t.chunks);
-  if (run && range.first < range.last) {
+  if (run && any) {
     const float bc1 = -expm1f((float)step * a.ln_b1), bc2 = -expm1f((float)step * a.ln_b2);
     sc.lr1 = sc.lr / bc1;
     sc.rbc2 = 1.0f / sqrtf(bc2);
     sc.key = mix(a.seed + (uint32_t)step * 0x9E3779B9u);
     if constexpr (BITS == 8) {
-      update_range_staged(t, a, sc, range);
+      update_range_staged(stages, t, a, sc, range, k0);
     } else {
-      for (int c = range.first, k = find_tensor(t, range.first); c < range.last; ++k) {
+      for (int c = range.first, k = k0; c < range.last; ++k) {
         const AdamEntry& e = t.e[k];
         const int end = min(range.last, k + 1 < t.n ? t.first[k + 1] : t.chunks);
         int64_t i = (int64_t)(c - t.first[k]) * kChunk + threadIdx.x * 8;
@@ -654,6 +681,9 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
         }
       }
     }
+  }
+  if constexpr (BITS == 8) {
+    if (!run && any && threadIdx.x == 0) mbar_wait(&stages.full[0], 0);  // a skipped step's copies have landed
   }
   // The last CTA of the call's last launch counts the step: by then every CTA has read the count.
   if (last) {
@@ -735,6 +765,7 @@ cudaError_t launch_norm(const Grads& grads, int n_tensors, int most, double* par
 template <int BITS, int MAX>
 cudaError_t launch_adamw(const AdamArgs& a, const dora_adamw_tensor_t* tensors, int n_tensors, int& i,
                          dora_adamw_control_t* control, const float* grad_scale, cudaStream_t st) {
+  const bool early = i == 0 && a.parts > 0;
   AdamTable<MAX> t;
   t.n = t.chunks = 0;
   for (; i < n_tensors && t.n < MAX; ++i) {
@@ -751,7 +782,7 @@ cudaError_t launch_adamw(const AdamArgs& a, const dora_adamw_tensor_t* tensors, 
   const int blocks = std::max(1, std::min(t.chunks, device_sm_count() * 4));
   ProfRange pr(BITS == 8 ? "adamw8" : "adamw32", st);
   return launch_pdl(adamw_kernel<BITS, MAX>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, a, control, grad_scale,
-                    i == n_tensors ? 1 : 0);
+                    early ? 1 : 0, i == n_tensors ? 1 : 0);
 }
 
 }  // namespace
