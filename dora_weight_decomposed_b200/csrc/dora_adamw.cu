@@ -5,7 +5,11 @@
 //
 // Both stream their tensors once and are bound by HBM. A work item is a chunk
 // of 2048 consecutive elements of one tensor, 8 per thread; a persistent grid
-// walks the chunks of all tensors in turn.
+// walks the chunks of all tensors in turn. Measured at 100 M elements with bf16
+// gradients: the norm 35 us (5.6 TB/s; 49 right behind an update, whose dirty
+// lines leave L2 meanwhile), the 8-bit update with a master copy 288 us and the
+// 32-bit one 522 us (5.6 and 5.4 TB/s). Without a master copy the 8-bit update is bound
+// by its instructions instead (17 M elements 48 us, 3.7 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <string>
