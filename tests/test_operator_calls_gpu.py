@@ -168,3 +168,33 @@ def test_profiler_names_the_kernels():
     names = [n for n, _ in dw.dora_profile_read()]
     dw.dora_profile_stop()
     assert names == ["fp8_quantize_rows", "fp8_forward", "fp8_backward", "grad_norm_partial", "adamw32"]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("numel", [3_000, 400_000, 9_000_000])
+def test_steps_in_a_row_and_fresh_parameters(numel, bits):
+    """Clipped steps right behind one another, and behind kernels that have just written the parameters and gradients,
+    give the bits of steps with a wait before each: an update reads nothing ahead of the work before it."""
+    gen = torch.Generator(device="cuda").manual_seed(numel + bits)
+    p0 = torch.randn(numel, generator=gen, device="cuda").to(BF)
+    gs = [torch.randn(numel, generator=gen, device="cuda").to(BF) for _ in range(3)]
+
+    def run(wait):
+        p, g = p0.clone(), gs[0].clone()
+        opt = dw.DoraAdamW([p], [g], lr=0.01, state_bits=bits, master=False)
+        norms = []
+        torch.cuda.synchronize()
+        for i in range(12):
+            g.copy_(gs[i % 3])
+            if i % 4 == 3:
+                p.mul_(0.5)
+            if wait:
+                torch.cuda.synchronize()
+            norms.append(opt.step(max_norm=1.0))
+            if i % 5 == 4:
+                norms.append(opt.step(max_norm=2.0))
+        state = opt.state_dict()
+        return [p, torch.stack(norms)] + [v.view(torch.uint8) for v in (state["avg"], state["sq"])]
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
