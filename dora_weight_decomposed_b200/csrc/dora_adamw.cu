@@ -379,13 +379,21 @@ __device__ __forceinline__ float2 quotient(float2 a, float minus_b, float inv_b)
   return fma2(fma2(q, both(minus_b), a), both(inv_b), q);
 }
 
-// sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2 (to the last place); zero for v = 0, NaN for inf.
+// sqrt(v) = v rsqrt(v) with one Newton step on the residual v - s^2, to the last place for v >= kRootLeast. Zero for
+// v = 0, NaN for inf, and below sqrt(kRootLeast) for the v between, where the estimate is held back: see root_small.
+constexpr float kRootLeast = 1e-37f;
 __device__ __forceinline__ float2 root(float2 v) {
   float2 y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1e-37f)));
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1e-37f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, kRootLeast)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, kRootLeast)));
   const float2 s = mul2(v, y);
   return fma2(fma2(mul2(s, both(-1.0f)), s, v), mul2(y, both(0.5f)), s);
+}
+
+// r with the roots of the v under kRootLeast, subnormal ones among them: those are scaled by 2^64, their roots by 2^-32.
+__device__ __forceinline__ float2 root_small(float2 v, float2 r) {
+  const float2 s = mul2(root(mul2(v, both(18446744073709551616.0f))), both(2.3283064365386963e-10f));
+  return make_float2(v.x < kRootLeast ? s.x : r.x, v.y < kRootLeast ? s.y : r.y);
 }
 
 __device__ __forceinline__ float reciprocal(float v) {
@@ -477,6 +485,13 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     r[j] = root(v[j]);
     if (BITS == 32) top = fmaxf(top, fmaxf(v[j].x, v[j].y));
   }
+  float least = fminf(fminf(r[0].x, r[0].y), fminf(r[1].x, r[1].y));
+  least = fminf(least, fminf(fminf(r[2].x, r[2].y), fminf(r[3].x, r[3].y)));
+  const bool some_zero = !(least > 0.f);
+  if (least < 3.2e-19f) {  // sqrt(kRootLeast) and its rounding: rare but for zero moments
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = root_small(v[j], r[j]);
+  }
   if (BITS == 8) {
     sm = moment_scale(m);
     sr = moment_scale(r);
@@ -507,9 +522,6 @@ __device__ __forceinline__ void update(const AdamEntry& e, const AdamArgs& a, co
     const uint32_t pair0 = e.index0 + (uint32_t)(i >> 1);
     // sqrt(v) > 0 is held as code 1 at least: t = 2^-6 (1 + 1 / 8).
     constexpr float kOne = 0.017578125f;
-    float least = fminf(fminf(r[0].x, r[0].y), fminf(r[1].x, r[1].y));
-    least = fminf(least, fminf(fminf(r[2].x, r[2].y), fminf(r[3].x, r[3].y)));
-    const bool some_zero = !(least > 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t h = mix((pair0 + j) ^ c.key);
