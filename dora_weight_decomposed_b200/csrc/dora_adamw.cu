@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_partial_kernel(const __gri
   }
 }
 
-// sqrt of the sum of the partial sums (the whole block takes part; every block gets the same value), and the scale.
+// sqrt of the sum of the partial sums (the whole block takes part; every block gets the same value), and the scale. A
+// norm that fp32 holds as infinite counts as not finite: the scale agrees with the norm that the caller reads.
 struct NormScale {
   double norm;
   float scale;
@@ -309,7 +310,7 @@ __device__ __forceinline__ NormScale norm_and_scale(const double* part, int n, f
   for (int w = 0; w < kThreads / 32; ++w) s += red[w];
   s = sqrt(s);
   const double c = (double)max_norm / (s + 1e-6);
-  return {s, !isfinite(s) ? __uint_as_float(0x7fffffffu) : (float)(c < 1.0 ? c : 1.0)};
+  return {s, !isfinite((float)s) ? __uint_as_float(0x7fffffffu) : (float)(c < 1.0 ? c : 1.0)};
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double* __restrict__ part, int n, float max_norm,

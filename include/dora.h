@@ -305,7 +305,8 @@ DORA_API dora_status_t dora_fp8_backward(const dora_fp8_desc_t* desc, int64_t T,
  *     norm  = sqrt(sum over all tensors of g^2)
  *     scale = min(1, max_norm / (norm + 1e-6)); NaN when the norm is not finite
  *   max_norm = +inf gives scale 1. norm and scale are one fp32 each in device
- *   memory. Sums are taken in double above 256 values, in a fixed order.
+ *   memory; a norm beyond fp32 is infinite. Sums are taken in double above 8
+ *   values, in a fixed order.
  *   Workspace: dora_grad_norm_workspace_size(n_tensors).
  *
  * dora_adamw: one AdamW step t = control->step + 1,

@@ -1,4 +1,4 @@
-"""The AdamW step at the ends of fp32's range: squares of gradients that are subnormal.
+"""The AdamW step at the ends of fp32's range: squares of gradients that are subnormal, norms beyond the type.
 
 Bounds, with h = 2^-24: v' = beta2 v + (1 - beta2) g'^2 takes at most eight roundings of h (two of them of a moment
 held in 8 bits, which is squared), and each of its terms, squares and sums may be subnormal and is then off by half the
@@ -97,3 +97,19 @@ def test_zero_gradients_among_tiny_ones(bits):
     s = opt.state_dict()
     assert (p[::3] == 1).all() and (host(s["sq"])[:n:3] == 0).all() and (host(s["avg"])[:n:3] == 0).all()
     assert (p[1::3] != 1).all() and (host(s["sq"])[1:n:3] > 0).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_norm_beyond_the_type_skips_the_step(bits):
+    """The norm of 1000 gradients of 3e38 is 9.5e39: it is returned as infinite, so it counts as infinite."""
+    g = torch.full((1000,), 3e38, device="cuda")
+    norm, scale = dw.dora_grad_norm([g], 1.0)
+    assert torch.isinf(norm) and torch.isnan(scale)
+    p = torch.ones(1000, device="cuda")
+    opt = dw.DoraAdamW([p], [g], lr=LR, state_bits=bits)
+    assert torch.isinf(opt.step(max_norm=1.0))
+    assert (p == 1).all() and int(opt.state_dict()["step"]) == 0
+    g.mul_(0.01)  # 9.5e37, inside the type
+    norm, scale = dw.dora_grad_norm([g], 1.0)
+    assert abs(float(norm) / (float(g[0]) * np.sqrt(1000.0)) - 1) <= 6 * H and float(scale) > 0
+    assert torch.isfinite(opt.step(max_norm=1.0)) and (p != 1).all()
