@@ -189,8 +189,15 @@ int sm_count(int dev) {
   return n;
 }
 
+template <int NT, bool W_MN, class XT>
+cudaError_t narrow_smem() {
+  static std::atomic<unsigned long long> set{0};
+  return set_smem_once(set, fp8_narrow_kernel<NT, W_MN, XT>, Fp8Narrow<NT>::SMEM_BYTES);
+}
+
 // Clusters of cs CTAs, one CTA per SM, that the current device holds at once (a cluster has to fit in one GPC): the
-// answer of the occupancy query, which counts one CTA per SM for the narrow kernels.
+// answer of the occupancy query, which counts one CTA per SM for the narrow kernels. The query knows the kernel by its
+// shared-memory limit, so that is raised first (before, it says 0). 0: no answer.
 template <int NT, bool W_MN>
 int clusters_alone(int cs, int sms) {
   cudaLaunchConfig_t cfg = {};
@@ -204,9 +211,10 @@ int clusters_alone(int cs, int sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, void>, &cfg) != cudaSuccess || n < 1) {
+  if (narrow_smem<NT, W_MN, void>() != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<NT, W_MN, void>, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    n = std::max(1, sms / cs * 7 / 8);
+    return 0;
   }
   return std::min(n, std::max(1, sms / cs));
 }
@@ -214,17 +222,32 @@ int clusters_alone(int cs, int sms) {
 // The same with the two CTAs per SM that run there (shared memory, registers and TMEM leave room for two): twice as
 // many. Seen in the times: 48 tiles in one wave with 5 splits and in two with 6, 96 tiles with 2 and 3. The small CTAs of
 // 16 tokens also fit as one cluster on every (cs + 1) / 2 SMs: 32 tiles with 8 splits in one wave, which at 128 tokens
-// (256 x 2048 x 2048) took 12.2 us, and 9.5 with 6. slots[cs], asked for once per device.
+// (256 x 2048 x 2048) took 12.2 us, and 9.5 with 6. Asked for once per device; where there is no answer (no device),
+// 7/8 of the SMs are assumed, for that call alone.
+struct NarrowSlots {
+  bool known = false;
+  int n[9] = {};
+};
 template <int NT, bool W_MN>
-const int* narrow_slots(int dev) {
-  static std::once_flag once[64];
-  static int slots[64][9];
-  std::call_once(once[dev], [&] {
-    int alone[9];
-    for (int cs = 1; cs <= 8; ++cs) alone[cs] = clusters_alone<NT, W_MN>(cs, sm_count(dev));
-    for (int cs = 1; cs <= 8; ++cs) slots[dev][cs] = std::max(2 * alone[cs], NT == 16 ? alone[(cs + 1) / 2] : 0);
-  });
-  return slots[dev];
+NarrowSlots narrow_slots(int dev) {
+  static std::mutex mu;
+  static NarrowSlots of[64];
+  std::lock_guard<std::mutex> lk(mu);
+  if (of[dev].known) return of[dev];
+  const int sms = sm_count(dev);
+  NarrowSlots s;
+  s.known = true;
+  int alone[9];
+  for (int cs = 1; cs <= 8; ++cs) {
+    alone[cs] = clusters_alone<NT, W_MN>(cs, sms);
+    if (alone[cs] < 1) {
+      s.known = false;
+      alone[cs] = std::max(1, sms / cs * 7 / 8);
+    }
+  }
+  for (int cs = 1; cs <= 8; ++cs) s.n[cs] = std::max(2 * alone[cs], NT == 16 ? alone[(cs + 1) / 2] : 0);
+  if (s.known) of[dev] = s;
+  return s;
 }
 
 // CTAs per tile of the narrow kernel (K splits, one cluster) and the call's estimated time in microseconds: waves of
@@ -241,10 +264,10 @@ template <int NT, bool W_MN>
 NarrowChoice narrow_choice(int dev, int64_t tiles, int64_t nkb, int64_t least = 1) {
   NarrowChoice best;
   const int sms = sm_count(dev);
-  const int* slots = narrow_slots<NT, W_MN>(dev);
+  const NarrowSlots slots = narrow_slots<NT, W_MN>(dev);
   for (int cs = (int)least; cs <= 8 && cs <= nkb; ++cs) {
     const double block = tiles * cs > sms ? 0.6 : 0.43, add = cs > 1 ? 2.0 + NT / 64.0 : 0.0;
-    const int64_t waves = cdiv(tiles, slots[cs]);
+    const int64_t waves = cdiv(tiles, slots.n[cs]);
     const double us = (double)waves * ((double)cdiv(nkb, cs) * block + add + 1.0) + 4.0;
     if (us < best.us - 1e-9) {
       best.us = us;
@@ -270,9 +293,7 @@ double pair_us(int dev, int64_t T, int64_t N, int64_t nkb) {
 
 template <int NT, bool W_MN, class XT>
 cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp8Geom& g, bool early_w, cudaStream_t st) {
-  auto kern = fp8_narrow_kernel<NT, W_MN, XT>;
-  static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, kern, Fp8Narrow<NT>::SMEM_BYTES);
+  const cudaError_t e = narrow_smem<NT, W_MN, XT>();
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(g.N, 128), t_tiles = cdiv(g.T, NT);
   // (The same splits for an x that comes in codes as for one that is quantised here: the same sums.)
@@ -292,7 +313,7 @@ cudaError_t launch_narrow(const CUtensorMap& tw, const CUtensorMap& tx, const Fp
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   ProfRange pr(W_MN ? "fp8_backward" : "fp8_forward", st);
-  return cudaLaunchKernelEx(&cfg, kern, tw, tx, g, cs, early_w ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<NT, W_MN, XT>, tw, tx, g, cs, early_w ? 1 : 0);
 }
 
 template <bool W_MN>
