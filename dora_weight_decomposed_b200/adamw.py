@@ -43,9 +43,14 @@ def _grad_table(grads, device):
                                               for i, g in enumerate(grads)])
 
 
-def _grad_norm(table, n: int, max_norm: float, norm, scale, ws, device, stream) -> None:
-    _check(load_library().dora_grad_norm(table, n, max_norm, norm.data_ptr(), scale.data_ptr(), _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(stream, device)))
+def _grad_norm(table, n: int, max_norm: float, ws, device, stream):
+    torch, lib = _torch(), load_library()
+    norm, scale = (_empty((), torch.float32, device, stream) for _ in range(2))
+    if ws is None:
+        ws = _empty(int(lib.dora_grad_norm_workspace_size(n)), torch.uint8, device, stream)
+    _check(lib.dora_grad_norm(table, n, max_norm, norm.data_ptr(), scale.data_ptr(), _ptr(ws),
+                              ws.numel() * ws.element_size(), _stream(stream, device)))
+    return norm, scale
 
 
 def dora_grad_norm(grads, max_norm: float = math.inf, *, ws=None, stream=None):
@@ -54,18 +59,12 @@ def dora_grad_norm(grads, max_norm: float = math.inf, *, ws=None, stream=None):
     norm = sqrt(sum of squares over all tensors); scale = min(1, max_norm /
     (norm + 1e-6)), NaN when the norm is not finite (DoraAdamW.step then skips).
     """
-    torch = _torch()
     grads = list(grads)
     if not grads:
         raise ValueError("grads is empty")
     device = grads[0].device
     _current(device)
-    table = _grad_table(grads, device)
-    norm, scale = (_empty((), torch.float32, device, stream) for _ in range(2))
-    if ws is None:
-        ws = _empty(int(load_library().dora_grad_norm_workspace_size(len(grads))), torch.uint8, device, stream)
-    _grad_norm(table, len(grads), float(max_norm), norm, scale, ws, device, stream)
-    return norm, scale
+    return _grad_norm(_grad_table(grads, device), len(grads), float(max_norm), ws, device, stream)
 
 
 class DoraAdamW:
@@ -155,12 +154,9 @@ class DoraAdamW:
         self._lr.fill_(float(lr))
 
     def grad_norm(self, max_norm: float = math.inf, *, stream=None):
-        """dora_grad_norm of the bound gradients."""
-        torch = _torch()
+        """dora_grad_norm of the bound gradients (with a workspace of its own: it may run beside a step)."""
         _current(self._device)
-        norm, scale = (_empty((), torch.float32, self._device, stream) for _ in range(2))
-        _grad_norm(self._grads, self._n, float(max_norm), norm, scale, self._ws, self._device, stream)
-        return norm, scale
+        return _grad_norm(self._grads, self._n, float(max_norm), None, self._device, stream)
 
     def step(self, *, max_norm: float | None = None, grad_scale=None, stream=None):
         """One step from the bound gradients; returns their norm when max_norm is given.
