@@ -188,14 +188,24 @@ class DoraAdamW:
         return {**self._state, "step": self._control[0]}
 
     def load_state_dict(self, state: dict) -> None:
-        """Copy a state_dict (or part of one) in; "step" may be an int. A master copy does not change the parameters."""
+        """Copy a state_dict (or part of one) in; "step" may be an int. A master copy does not change the parameters.
+
+        A state that is refused leaves the handle as it was.
+        """
+        step = None
         for k, v in state.items():
             if k == "step":
-                self._control[0].fill_(int(v))
+                step = int(v)
+                if step < 0:
+                    raise ValueError(f"step is {step}")
                 continue
             if k not in self._state:
                 raise KeyError(f"no state {k!r} here (have {sorted(self._state)})")
             mine = self._state[k]
             if v.shape != mine.shape or v.dtype != mine.dtype:
                 raise ValueError(f"{k} is {v.dtype} {tuple(v.shape)}, expected {mine.dtype} {tuple(mine.shape)}")
-            mine.copy_(v)
+        for k, v in state.items():
+            if k != "step":
+                self._state[k].copy_(v)
+        if step is not None:
+            self._control[0].fill_(step)

@@ -34,3 +34,29 @@ def test_a_norm_on_the_side_leaves_the_steps_workspace():
     torch.cuda.synchronize()
     assert (opt._ws == 7).all()
     assert all(torch.equal(n, want) for n in norms)
+
+
+def snapshot(opt):
+    return {k: v.clone().view(torch.uint8) if v.element_size() == 1 else v.clone() for k, v in opt.state_dict().items()}
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad,error", [
+    (lambda s: {"step": 3, "avg": s["avg"], "nothing": s["sq"]}, KeyError),
+    (lambda s: {"step": 3, "avg": s["avg"], "sq": s["sq"][1:]}, ValueError),
+    (lambda s: {"avg": s["avg"], "sq": s["sq"].float().double()}, ValueError),
+    (lambda s: {"avg": s["avg"], "step": -1}, ValueError)])
+def test_a_refused_load_changes_nothing(bits, bad, error):
+    _, _, a = handle(bits)
+    a.step()
+    state = {k: v.clone() for k, v in a.state_dict().items()}
+    params, _, b = handle(bits)
+    before, p0 = snapshot(b), [p.clone() for p in params]
+    with pytest.raises(error):
+        b.load_state_dict(bad(state))
+    after = snapshot(b)
+    assert all(torch.equal(before[k], after[k]) for k in before)
+    b.load_state_dict(state)  # the whole of it loads, and steps go on from there
+    assert int(b.state_dict()["step"]) == 1 and all(torch.equal(x, y) for x, y in zip(params, p0))
+    b.step()
+    assert int(b.state_dict()["step"]) == 2
