@@ -64,6 +64,8 @@ def dora_grad_norm(grads, max_norm: float = math.inf, *, ws=None, stream=None):
         raise ValueError("grads is empty")
     device = grads[0].device
     _current(device)
+    if ws is not None and ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
     return _grad_norm(_grad_table(grads, device), len(grads), float(max_norm), ws, device, stream)
 
 
