@@ -343,7 +343,7 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8
   }();
   if (regs < kF8LaunchRegs) return cudaErrorInvalidKernelImage;
   const int64_t pairs = std::min<int64_t>(cdiv(g.T, 256) * cdiv(g.N, 256), std::max(1, sm_count(this_device()) / 2));
-  ProfRange pr(B_MN ? "fp8_backward" : "fp8_forward", st);
+  ProfRange pr(B_MN ? "fp8_backward_pairs" : "fp8_forward_pairs", st);
   return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kF8PairThreads), kF8PairSmem, st, ta, tb, tout, g);
 }
 
