@@ -113,3 +113,34 @@ def test_a_norm_beyond_the_type_skips_the_step(bits):
     norm, scale = dw.dora_grad_norm([g], 1.0)
     assert abs(float(norm) / (float(g[0]) * np.sqrt(1000.0)) - 1) <= 6 * H and float(scale) > 0
     assert torch.isfinite(opt.step(max_norm=1.0)) and (p != 1).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_moment_that_is_not_finite(bits):
+    """A gradient of 3e19 has an infinite square. In 32 bits its element stands still from then on; in 8 bits its block of
+    128 shares the scale, and is NaN from the next step on. Every other block goes on as without it."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    g0 = torch.randn(4096, generator=gen, device="cuda")
+    res = []
+    for bad in (False, True):
+        p, g = torch.ones(4096, device="cuda"), g0.clone()
+        if bad:
+            g[2100] = 3e19
+        opt = dw.DoraAdamW([p], [g], lr=LR, state_bits=bits, seed=1)
+        opt.step()
+        first = p.clone()
+        assert bool(torch.isfinite(first).all())
+        g.copy_(g0)
+        opt.step()
+        res.append((first, p))
+    (f0, p0), (f1, p1) = res
+    keep = torch.ones(4096, dtype=torch.bool, device="cuda")
+    keep[2048:2176] = False
+    assert torch.equal(p0[keep], p1[keep]) and float(f1[2100]) == 1.0
+    if bits == 32:
+        assert float(p1[2100]) == 1.0
+        keep = torch.ones(4096, dtype=torch.bool, device="cuda")
+        keep[2100] = False
+        assert torch.equal(p0[keep], p1[keep])
+    else:
+        assert bool(torch.isnan(p1[2048:2176]).all())
