@@ -2,11 +2,13 @@
 //
 //   out[t, n] = sum_kb xs[kb, t] ws[n / 128, kb] sum_{k in kb} xq[t, k] wq[n, k]
 //
-// The scales change every 128 values of K, so the tensor cores' accumulator
-// holds one k-block at a time: the four MMAs of a k-block write a fresh
-// accumulator in TMEM, and the epilogue warps fold it into fp32 sums in
-// registers, one multiply-add per value with the row's scale times the
-// tile's. Two accumulators let the MMAs of the next k-block run meanwhile.
+// Scales that are powers of two (all that dora_fp8_quantize makes) are applied
+// by the tensor cores, from exponent bytes in TMEM, and one accumulator holds
+// the whole sum. Other scales change every 128 values of K, so an accumulator
+// then holds one k-block at a time: the four MMAs of a k-block write a fresh
+// one, and the epilogue warps fold it into fp32 sums in registers, one
+// multiply-add per value with the row's scale times the tile's. Two
+// accumulators let the MMAs of the next k-block run meanwhile.
 #pragma once
 
 #include <type_traits>
@@ -125,7 +127,8 @@ struct Fp8Geom {
 };
 
 // A scale that the tensor cores can apply: a positive normal power of two; or a non-finite scale of x, which stands for
-// NaN there and makes its row's results NaN either way.
+// NaN there. Its row's results are not finite either way: the quantiser's codes under such a scale make NaN, other codes
+// under an infinite one would make infinities where the scale is applied in fp32.
 __device__ __forceinline__ bool is_power(float s) {
   const uint32_t u = __float_as_uint(s);
   return (u & 0x807fffffu) == 0 && u != 0 && u < 0x7f800000u;
@@ -575,7 +578,8 @@ static_assert(kF8PairSmem <= 227 * 1024, "shared memory");
 
 // Tiles in groups of 16 rows of tiles, rows fastest: the tiles in flight share operands in L2, and neighbours the
 // weight's. (T = 4096 of 8192 x 8192, run for a second: 256 us, 262 in groups of 8, 270 of 4, 276 of 2; groups of
-// columns 259 to 276.)
+// columns 259 to 276. T = 8192 of 27648 x 5120 1072 against 1095 us in groups of 8; T = 16384 of 4096 x 4096 loses by
+// it, 273.5 against 270.)
 constexpr int kF8TileGroup = 16;
 __device__ __forceinline__ void fp8_tile_coords(int t, int m_tiles, int n_tiles, int& m, int& n) {
   const int per_group = kF8TileGroup * n_tiles;

@@ -40,8 +40,12 @@ __device__ __forceinline__ void flag_timeout() { atomicOr(&g_device_status, DORA
 // the next kernel in the stream start launching once every CTA of this grid
 // has started (no CTA of this grid can then be left waiting for an SM);
 // pdl_wait blocks until the previous grid has completed and its memory
-// writes are visible. Every kernel here calls pdl_wait before its first
-// global-memory access. Both are no-ops without a programmatic dependency.
+// writes are visible. Every kernel calls pdl_wait before its first
+// global-memory access, but for two that read ahead what the grid before them
+// does not write: fp8_narrow_kernel the weight, behind the quantiser of x, and
+// adamw_kernel its first chunk, behind the gradient norm. Those two grids in
+// front trigger only after their own pdl_wait, so all work before them is done
+// when the reads begin. Both calls are no-ops without a programmatic dependency.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
