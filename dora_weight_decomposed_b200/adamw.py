@@ -80,6 +80,9 @@ class DoraAdamW:
         stochastically from `seed`).
     master: keep a float32 copy of every bf16 parameter and round the parameter
         from it; without it a bf16 parameter loses updates under half its spacing.
+
+    The state is made on the current stream: a step on another one is ordered
+    behind that by the caller, who also keeps the handle until its steps are done.
     """
 
     def __init__(self, params, grads, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,

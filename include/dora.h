@@ -316,7 +316,8 @@ DORA_API dora_status_t dora_fp8_backward(const dora_fp8_desc_t* desc, int64_t T,
  *     g' = grad_scale g      (grad_scale NULL: 1)
  *     m' = beta1 m + (1 - beta1) g',   v' = beta2 v + (1 - beta2) g'^2
  *     p' = p - lr wd p - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
- *   in fp32 whatever the tensors' type. A master copy (fp32) holds p where
+ *   in fp32 whatever the tensors' type (eps = 0 divides by zero where v' is
+ *   zero, as it is for |g'| below about 1e-21 from a zero state). A master copy (fp32) holds p where
  *   given; param is then p' rounded to nearest. state_bits = 32: exp_avg = m
  *   and exp_avg_sq = v in fp32. state_bits = 8: exp_avg holds m and exp_avg_sq
  *   holds sqrt(v) as e4m3 codes in blocks of 128 consecutive elements, value =

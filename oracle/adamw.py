@@ -7,9 +7,11 @@ from . import fp8
 
 
 def grad_norm(grads, max_norm=np.inf):
-    """(norm, scale): scale = min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite."""
+    """(norm, scale): scale = min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite in float32."""
     norm = np.sqrt(sum(float(np.sum(np.asarray(g, np.float64) ** 2)) for g in grads))
-    return norm, min(1.0, max_norm / (norm + 1e-6)) if np.isfinite(norm) else np.nan
+    with np.errstate(over="ignore"):
+        finite = np.isfinite(np.float32(norm))
+    return norm, min(1.0, max_norm / (norm + 1e-6)) if finite else np.nan
 
 
 def step(p, g, m, v, t, *, lr, betas, eps, weight_decay, scale=1.0):
